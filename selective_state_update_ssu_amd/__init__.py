@@ -20,6 +20,10 @@ kernel. There is no fallback: without the built library every call raises.
                             return_intermediate_states, state_dtype, workspace,
                             static_scratch)
 
+    causal_conv1d_varlen, causal_conv1d_update, selective_scan_varlen,
+    selective_scan_update, cache_alloc, cache_free, cache_retain, cache_copy, cache_fork,
+    cache_compact: the operators around the update (layer.py, include/layer.h)
+
 Operand shapes follow the MATE documentation page "Source code for mate.mamba"
 (`selective_state_update`): state [slots, heads, dim, dstate]; x, z, out
 [rows, heads, dim]; dt [rows, heads], [rows, heads, 1] or [rows, heads, dim]
@@ -719,3 +723,11 @@ def ssd_combined_fwd_varlen(x, dt, A, B, C, chunk_size, cu_seqlens, cu_chunk_seq
     if rc != _abi.SSU_OK:
         _raise(lib, rc, entry.__name__)
     return states
+
+
+# ---------------------------------------------- the operators around the update
+
+from . import layer  # noqa: E402
+from .layer import *  # noqa: E402,F401,F403
+
+__all__ += layer.__all__

@@ -1,4 +1,4 @@
-"""ctypes mirror of include/ssu.h and include/ssd.h. Field order and types must match the header;
+"""ctypes mirror of include/ssu.h, include/ssd.h and include/layer.h. Field order and types must match the header;
 the library checks `struct_size` on every call, so a stale mirror fails loudly."""
 import ctypes
 import os
@@ -13,6 +13,10 @@ ABI_VERSION = 1
 EXPORTS = ("ssu_one_token", "ssu_packed_varlen", "ssu_ring_update", "ssu_ring_commit",
            "ssu_last_error", "ssu_version", "ssu_ssd_workspace_bytes", "ssu_ssd_prefill",
            "ssu_ssd_prefill_noalloc")
+# include/layer.h
+LAYER_EXPORTS = ("ssu_conv1d_varlen", "ssu_conv1d_update", "ssu_scan_workspace_bytes",
+                 "ssu_scan_varlen", "ssu_scan_update", "ssu_cache_alloc", "ssu_cache_adjust",
+                 "ssu_cache_copy", "ssu_cache_compact")
 
 
 class Operands(ctypes.Structure):
@@ -79,6 +83,50 @@ class SsdArgs(ctypes.Structure):
     ]
 
 
+class ConvArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", c_uint32), ("io_dtype", c_int32),
+        ("conv_state", c_void_p), ("nslots", c_int64), ("slot_stride", c_int64),
+        ("x", c_void_p), ("x_stride", c_int64), ("out", c_void_p), ("out_stride", c_int64),
+        ("weight", c_void_p), ("bias", c_void_p), ("rows", c_int64), ("dim", c_int64),
+        ("width", c_int32), ("silu", c_int32),
+        ("cu_seqlens", c_void_p), ("cu_dtype", c_int32), ("slot_dtype", c_int32),
+        ("nseq", c_int64), ("has_initial", c_void_p), ("slots", c_void_p),
+        ("pad_slot_id", c_int64),
+    ]
+
+
+class ScanArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", c_uint32), ("state_dtype", c_int32),
+        ("state", c_void_p), ("nslots", c_int64), ("slot_stride", c_int64),
+        ("rows", c_int64), ("dim", c_int64), ("dstate", c_int64), ("ngroups", c_int64),
+        ("x", c_void_p), ("z", c_void_p), ("dt", c_void_p), ("B", c_void_p), ("C", c_void_p),
+        ("out", c_void_p),
+        ("x_stride", c_int64), ("z_stride", c_int64), ("dt_stride", c_int64),
+        ("B_stride", c_int64), ("C_stride", c_int64), ("out_stride", c_int64),
+        ("io_dtype", c_int32), ("dt_dtype", c_int32),
+        ("A", c_void_p), ("D", c_void_p), ("dt_bias", c_void_p),
+        ("dt_softplus", c_int32), ("cu_dtype", c_int32), ("cu_seqlens", c_void_p),
+        ("nseq", c_int64), ("has_initial", c_void_p), ("slots", c_void_p),
+        ("slot_dtype", c_int32), ("reserved", c_int32), ("pad_slot_id", c_int64),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+    ]
+
+
+class CacheBlock(ctypes.Structure):
+    _fields_ = [("base", c_void_p), ("slot_bytes", c_int64), ("stride_bytes", c_int64)]
+
+
+class CacheArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", c_uint32), ("delta", c_int32), ("refcount", c_void_p),
+        ("nslots", c_int64), ("caches", ctypes.POINTER(CacheBlock)), ("ncaches", c_int64),
+        ("src", c_void_p), ("dst", c_void_p), ("src_dtype", c_int32), ("dst_dtype", c_int32),
+        ("n", c_int64), ("ids", c_void_p), ("remap", c_void_p), ("plan", c_void_p),
+    ]
+
+
 def load(path: str) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise RuntimeError(
@@ -98,6 +146,14 @@ def load(path: str) -> ctypes.CDLL:
     for f in (lib.ssu_ssd_prefill, lib.ssu_ssd_prefill_noalloc):
         f.restype = c_int32
         f.argtypes = [ctypes.POINTER(SsdArgs), c_void_p]
+    for f, args in ((lib.ssu_conv1d_varlen, ConvArgs), (lib.ssu_conv1d_update, ConvArgs),
+                    (lib.ssu_scan_varlen, ScanArgs), (lib.ssu_scan_update, ScanArgs),
+                    (lib.ssu_cache_alloc, CacheArgs), (lib.ssu_cache_adjust, CacheArgs),
+                    (lib.ssu_cache_copy, CacheArgs), (lib.ssu_cache_compact, CacheArgs)):
+        f.restype = c_int32
+        f.argtypes = [ctypes.POINTER(args), c_void_p]
+    lib.ssu_scan_workspace_bytes.restype = c_size_t
+    lib.ssu_scan_workspace_bytes.argtypes = [c_int64] * 5
     lib.ssu_last_error.restype = c_char_p
     lib.ssu_last_error.argtypes = []
     lib.ssu_version.restype = c_int32

@@ -1,0 +1,125 @@
+// layer_common.hpp -- what the kernels and front ends of the layer operators
+// (include/layer.h) share: element access by storage type, the search for a
+// packed row's sequence, and host-side checks of argument structs.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "layer.h"
+#include "ssu_kernel.hpp"
+#include "ssu_launch.h"
+
+namespace layer {
+
+using ssu::Bits;
+using ssu::Pack;
+using ssu::Words;
+using ssu::group_sum;
+using ssu::lds_barrier;
+using ssu::load_index;
+using ssu::widen_io;
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// VEC consecutive elements of storage type T as 32-bit words (one 16-bit value in
+// a half word when VEC is 1), moved by one vector-memory instruction.
+template <typename T, int VEC>
+struct Raw {
+    static constexpr int kWords = VEC * static_cast<int>(sizeof(T)) / 4;
+    typedef typename ssu::Words<kWords>::type type;
+    static __device__ __forceinline__ type load(const T* p) {
+        return *reinterpret_cast<const type*>(p);
+    }
+    static __device__ __forceinline__ void store(T* p, type v) { *reinterpret_cast<type*>(p) = v; }
+    static __device__ __forceinline__ void widen(type v, float (&f)[VEC]) {
+        constexpr int per = ssu::Pack<T>::kPerWord;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) ssu::Pack<T>::widen(word(v, i), &f[i * per]);
+    }
+    static __device__ __forceinline__ type narrow(const float (&f)[VEC]) {
+        constexpr int per = ssu::Pack<T>::kPerWord;
+        type v;
+        if constexpr (kWords == 1) {
+            v[0] = ssu::Pack<T>::narrow(&f[0]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) v[i] = ssu::Pack<T>::narrow(&f[i * per]);
+        }
+        return v;
+    }
+    static __device__ __forceinline__ unsigned word(type v, int i) { return v[i]; }
+};
+
+template <typename T>
+struct Raw<T, 1> {
+    typedef typename ssu::Bits<T>::type type;
+    static __device__ __forceinline__ type load(const T* p) {
+        return *reinterpret_cast<const type*>(p);
+    }
+    static __device__ __forceinline__ void store(T* p, type v) { *reinterpret_cast<type*>(p) = v; }
+    static __device__ __forceinline__ void widen(type v, float (&f)[1]) {
+        f[0] = ssu::widen_io<T>(v);
+    }
+    static __device__ __forceinline__ type narrow(const float (&f)[1]) {
+        return __builtin_bit_cast(type, static_cast<T>(f[0]));
+    }
+};
+
+// v * sigmoid(v) with the hardware's exp2 and reciprocal (each within about one
+// unit in the last place, far below one rounding of a 16-bit result; an fp32 result is
+// off by a few 2^-24 relative). Minus infinity gives NaN as the formula does.
+__device__ __forceinline__ float silu_fast(float v) {
+    return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * v));
+}
+
+// The number of entries i < n of the non-decreasing cu with cu[i] <= row, found by
+// the whole wave: every step probes 64 entries and keeps the interval between two
+// of them, so it ends for any content of cu.
+__device__ __forceinline__ int64_t count_starts(const void* cu, int is64, int64_t n, int64_t row) {
+    const int lane = threadIdx.x & 63;
+    int64_t lo = 0, hi = n;
+    while (lo < hi) {
+        const int64_t step = (hi - lo + 63) / 64;
+        const int64_t i = lo + lane * step;
+        const bool in = i < hi && load_index(cu, is64, i) <= row;
+        const int c = __builtin_popcountll(__ballot(in));
+        if (step == 1) return lo + c;
+        if (c == 0) return lo;
+        hi = lo + c * step < hi ? lo + c * step : hi;
+        lo += (c - 1) * step + 1;
+    }
+    return lo;
+}
+
+// ------------------------------------------------------------------ host checks
+
+inline bool is_dtype(int32_t d) { return d == SSU_F32 || d == SSU_F16 || d == SSU_BF16; }
+inline bool is_index(int32_t d) { return d == SSU_I32 || d == SSU_I64; }
+inline int64_t size_of(int32_t d) { return d == SSU_F32 ? 4 : 2; }
+inline bool aligned(const void* p, int64_t a) {
+    return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(a) == 0;
+}
+
+// Whether [a, a + abytes) and [b, b + bbytes) share a byte.
+inline bool overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
+    if (!a || !b || abytes <= 0 || bbytes <= 0) return false;
+    const auto a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return a0 < b0 + static_cast<uintptr_t>(bbytes) && b0 < a0 + static_cast<uintptr_t>(abytes);
+}
+
+// Bytes that `rows` rows of `width` elements, `stride` elements apart, span.
+inline int64_t span(int64_t rows, int64_t stride, int64_t width, int64_t esz) {
+    return rows > 0 ? ((rows - 1) * stride + width) * esz : 0;
+}
+
+inline int launched(const char* entry) {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return ssu::report(SSU_ERR_LAUNCH, "%s: launch failed: %s", entry, hipGetErrorString(e));
+    return ssu::report_ok();
+}
+
+}  // namespace layer
