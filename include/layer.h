@@ -103,7 +103,8 @@ typedef struct ssu_scan_args {
     int32_t slot_dtype;        /* ssu_index_dtype */
     int32_t reserved;          /* 0 */
     int64_t pad_slot_id;
-    void *workspace;           /* varlen: ssu_scan_workspace_bytes(...) bytes, 256-byte aligned */
+    void *workspace;           /* varlen: ssu_scan_workspace_bytes(...) bytes, 256-byte
+                                  aligned; may be NULL if that is 0 */
     size_t workspace_bytes;
 } ssu_scan_args;
 

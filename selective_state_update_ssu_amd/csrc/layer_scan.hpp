@@ -3,17 +3,16 @@
 //
 // Prompts. The recurrence is serial in time and independent over channels and
 // state elements, so a lane owns one channel, a wave 64 adjacent channels of one
-// group and a quarter of their state elements (an eighth of 256), and a workgroup of
-// four waves (eight) one piece of a sequence. Decays never leave registers; per element and row the work
-// is five vector instructions, one of them an exponential at half rate:
+// group and a quarter of their state elements (an eighth of 128 and 256), and a workgroup of
+// four waves (eight) one piece of a sequence. Decays never leave registers; per element
+// and row the work is five vector instructions, one of them an exponential at half rate:
 //     a = v A;  e = 2^a;  u = v x B;  s = e s + u;  y += C s
-// which is what bounds it (A is scaled by log2 e once). B and C are the same for
-// the whole wave: a first kernel widens them to fp32 in the order the waves take
-// them, and the scan reads them through the scalar cache into scalar registers, the
-// operands that a vector instruction takes besides its lanes' own for nothing.
-// The lanes' v and v x (softplus once per row and channel) pass through LDS, a tile
-// of kTile rows at a time: each wave prepares its share of the tile's rows for all, and
-// later sums the waves' partial y of the same rows, gates and stores them.
+// which is what bounds it (A is scaled by log2 e once). What the waves share passes
+// through LDS a tile of kTile rows at a time: B and C, widened to fp32 and read back by
+// broadcast; v and v x of every channel, of which each wave prepares its share of the
+// rows; and the waves' partial y, which the wave that prepared a row sums, gates and
+// stores. One barrier per tile: a tile is prepared, from inputs requested one tile earlier
+// still, while the tile before it is computed.
 //
 // Few sequences leave most of the card idle, so long ones are then cut into
 // pieces of `piece` rows: a first pass over all but a sequence's last piece finds
@@ -28,19 +27,18 @@
 
 namespace layer {
 
-constexpr int kTile = 16;  // rows staged at a time
+constexpr int kTile = 8;  // rows staged at a time
 
-// Waves of a workgroup, which share a channel's state elements: 64 elements per lane and
-// their decays would not fit the registers of four waves.
-__host__ __device__ constexpr int scan_waves(int dstate) { return dstate > 128 ? 8 : 4; }
+// Waves of a workgroup, which share a channel's state elements: with more than 16 elements
+// per lane (state and A in registers) a compute unit holds too few waves.
+__host__ __device__ constexpr int scan_waves(int dstate) { return dstate > 64 ? 8 : 4; }
 
 // One piece of one sequence. `seq` < 0: no work.
 struct Piece {
-    int32_t seq;
-    int32_t index;        // of this piece in its sequence
-    int32_t count;        // pieces of its sequence
-    int32_t rows;
+    int64_t seq;
+    int64_t index, count; // of this piece in its sequence, and its sequence's pieces
     int64_t row;          // first packed row
+    int rows;
 };
 
 struct ScanParams {
@@ -59,11 +57,9 @@ struct ScanParams {
     const void* slots;
     int64_t nslots, slot_stride, rows, nseq, pad_slot_id;
     int64_t x_stride, z_stride, dt_stride, B_stride, C_stride, out_stride;
-    int64_t piece;        // rows of a piece
-    int64_t pieces;       // entries of the table
-    // Scratch of the prompts' kernels.
-    Piece* table;         // [pieces], a sequence's pieces adjacent
-    float* bc;            // [rows][groups][waves][B: dstate / waves, C: dstate / waves]
+    int64_t piece;        // rows of a piece; 0: sequences are whole
+    int64_t pieces;       // pieces there may be
+    // Scratch of prompts in pieces, a sequence's pieces adjacent.
     float* ends;          // [pieces][dim][dstate]: end states; of a last piece: the entering state
     float* sums;          // [pieces][dim]: sum of v
     int32_t dim, ngroups, group_dim;
@@ -72,14 +68,13 @@ struct ScanParams {
     int32_t wide_bc;      // update: B and C can be read in 16-byte pieces
 };
 
-// log(1 + e^v). log1p(e) = log(1 + e) e / ((1 + e) - 1) cancels the rounding of
-// 1 + e (Goldberg, "What every computer scientist should know about floating-point
-// arithmetic", 1991, theorem 4).
+// log(1 + e^v). With u = 1 + e rounded, log1p(e) = log(u) + (e - (u - 1)) / u to first order
+// in the rounding e - (u - 1), which is exact; leaving out the 1 / u is off by less than
+// e 2^-24, a relative 2^-24.
 __device__ __forceinline__ float softplus_fast(float v) {
     const float e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(v));
-    const float u = 1.f + e, d = u - 1.f;
-    const float l = d == 0.f ? e : __builtin_amdgcn_logf(u) * kLn2 * (e * __builtin_amdgcn_rcpf(d));
-    return fmaxf(v, 0.f) + (v != v ? v : l);
+    const float u = 1.f + e;
+    return fmaxf(v, 0.f) + fmaf(__builtin_amdgcn_logf(u), kLn2, e - (u - 1.f));
 }
 
 // Element i of a state of storage type `dtype`, and its store (to nearest).
@@ -98,113 +93,156 @@ __device__ __forceinline__ void state_store(void* p, int dtype, int64_t i, float
         static_cast<__bf16*>(p)[i] = static_cast<__bf16>(v);
 }
 
-__device__ __forceinline__ int64_t scan_slot(const ScanParams& p, int64_t b) {
+template <typename P>
+__device__ __forceinline__ int64_t scan_slot(const P& p, int64_t b) {
     const int64_t s = p.slots ? load_index(p.slots, p.slot64, b) : b;
     return s != p.pad_slot_id && s >= 0 && s < p.nslots ? s : -1;
 }
 
-// Reads through the scalar cache.
-typedef __attribute__((address_space(4))) const float scalar_float;
-
-// Widens B and C of every row to fp32 in the scan's order; workgroup 0 also cuts the
-// sequences into pieces, in order, inert and empty ones into none.
-constexpr int kPrepThreads = 256;
-
-template <typename IT>
-__global__ __launch_bounds__(kPrepThreads) void scan_prepare_kernel(const ScanParams p, int dstate) {
-    if (blockIdx.x == 0) {
-        __shared__ int64_t base[kPrepThreads];
-        int64_t next = 0;
-        for (int64_t b0 = 0; b0 < p.nseq; b0 += kPrepThreads) {
-            const int64_t b = b0 + threadIdx.x;
-            int64_t begin = 0, len = 0;
-            if (b < p.nseq) {
-                begin = load_index(p.cu, p.cu64, b);
-                const int64_t end = load_index(p.cu, p.cu64, b + 1);
-                if (begin >= 0 && begin <= end && end <= p.rows && scan_slot(p, b) >= 0)
-                    len = end - begin;
-            }
-            const int64_t count = (len + p.piece - 1) / p.piece;
-            base[threadIdx.x] = count;
-            __syncthreads();
-            for (int step = 1; step < kPrepThreads; step *= 2) {
-                const int64_t add = threadIdx.x >= step ? base[threadIdx.x - step] : 0;
-                __syncthreads();
-                base[threadIdx.x] += add;
-                __syncthreads();
-            }
-            // The table holds every piece of non-decreasing cu_seqlens; a sequence of any
-            // others that does not fit is left out whole.
-            const int64_t at = next + base[threadIdx.x] - count;
-            const bool fits = at + count <= p.pieces;
-            for (int64_t k = 0; k < count && at + k < p.pieces; ++k) {
-                Piece q;
-                q.seq = fits ? static_cast<int32_t>(b) : -1;
-                q.index = static_cast<int32_t>(k);
-                q.count = static_cast<int32_t>(count);
-                q.rows = static_cast<int32_t>(len - k * p.piece < p.piece ? len - k * p.piece : p.piece);
-                q.row = begin + k * p.piece;
-                p.table[at + k] = q;
-            }
-            next += base[kPrepThreads - 1];
-            __syncthreads();
-        }
-        for (int64_t i = next + threadIdx.x; i < p.pieces; i += kPrepThreads) p.table[i].seq = -1;
-    }
-    const int per_row = p.ngroups * dstate;
-    const int waves = scan_waves(dstate), nw = dstate / waves;
-    const int64_t total = p.rows * per_row;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPrepThreads + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * kPrepThreads) {
-        const int64_t row = i / per_row;
-        const int gn = static_cast<int>(i % per_row);
-        const int g = gn / dstate, n = gn % dstate;
-        float* to = p.bc + ((row * p.ngroups + g) * waves + n / nw) * 2 * nw + n % nw;
-        to[0] = static_cast<float>(static_cast<const IT*>(p.B)[row * p.B_stride + gn]);
-        to[nw] = static_cast<float>(static_cast<const IT*>(p.C)[row * p.C_stride + gn]);
-    }
+// The kernel's parameters, read from the argument segment from here on: the compiler
+// otherwise loads all of them at the kernel's start, more than there are scalar registers
+// beside what finding the piece takes.
+typedef __attribute__((address_space(4))) const ScanParams scan_args;
+__device__ __forceinline__ scan_args* fresh_args() {
+    scan_args* a = (scan_args*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(a));
+    return a;
 }
 
-// A lane's inputs of the rows it prepares in one tile, as loaded.
-template <typename IT, int ROWS>
+// The rows of sequence b; none if it is inert.
+__device__ __forceinline__ int64_t sequence(const ScanParams& p, int64_t b, int64_t* begin) {
+    *begin = load_index(p.cu, p.cu64, b);
+    const int64_t end = load_index(p.cu, p.cu64, b + 1);
+    return *begin >= 0 && *begin <= end && end <= p.rows && scan_slot(p, b) >= 0 ? end - *begin : 0;
+}
+
+// Place of workgroup `id` of `n` in a list that goes from long to short work, when all
+// are resident at once: workgroups reach the compute units in rounds of kUnits, and every
+// second round takes its share of the list backwards, so that the shares of the units differ
+// little in sum. A bijection of [0, n).
+constexpr int kUnits = 256;
+__device__ __forceinline__ int fold(int id, int n) {
+    const int round = id / kUnits, at = id % kUnits;
+    if (round % 2 == 0 || (round + 1) * kUnits > n) return id;
+    // Consecutive workgroups go to consecutive XCDs: the unit on this XCD counted from the end.
+    return round * kUnits + (kUnits / ssu::kXcds - 1 - at / ssu::kXcds) * ssu::kXcds + at % ssu::kXcds;
+}
+
+// Piece `i` of the call, found by a whole wave from cu_seqlens. Whole sequences, up to 64 of
+// them, go from the longest to the shortest.
+__device__ __forceinline__ Piece find_piece(const ScanParams& p, int64_t i) {
+    const int lane = threadIdx.x & 63;
+    Piece q;
+    q.seq = -1;
+    q.index = 0;
+    q.count = 1;
+    q.row = 0;
+    q.rows = 0;
+    if (p.piece == 0) {
+        int64_t b = i;
+        if (p.nseq <= 64) {
+            int64_t begin, len = lane < p.nseq ? sequence(p, lane, &begin) : -1;
+            const int mine = static_cast<int>(len);
+            int rank = 0;
+            for (int j = 0; j < p.nseq; ++j) {
+                const int other = __builtin_amdgcn_readlane(mine, j);
+                rank += other > mine || (other == mine && j < lane);
+            }
+            b = __builtin_ctzll(__ballot(rank == i && lane < p.nseq) | 1ull << 63);
+        }
+        const int64_t len = sequence(p, b, &q.row);
+        if (len > 0) q.seq = b;
+        q.rows = static_cast<int>(len);
+    } else {
+        int64_t before = 0;  // pieces of the sequences before
+        for (int64_t b0 = 0; b0 < p.nseq; b0 += 64) {
+            int64_t begin = 0, len = b0 + lane < p.nseq ? sequence(p, b0 + lane, &begin) : 0;
+            const int piece_rows = static_cast<int>(p.piece);
+            const int count = (static_cast<int>(len) + piece_rows - 1) / piece_rows;
+            int upto = count;  // of lanes 0 .. lane
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const int o = __shfl_up(upto, d);
+                if (lane >= d) upto += o;
+            }
+            const unsigned long long past = __ballot(before + upto > i);
+            if (past) {
+                const int l = __builtin_ctzll(past);
+                q.seq = b0 + l;
+                q.count = __builtin_amdgcn_readlane(count, l);
+                q.index = i - before - __builtin_amdgcn_readlane(upto, l) + q.count;
+                len = sequence(p, q.seq, &begin);
+                q.row = begin + q.index * p.piece;
+                len -= q.index * p.piece;
+                q.rows = static_cast<int>(len < p.piece ? len : p.piece);
+                // Decreasing cu_seqlens may name more pieces than the scratch holds.
+                if (i - q.index + q.count > p.pieces) q.seq = -1;
+                break;
+            }
+            before += __builtin_amdgcn_readlane(upto, 63);
+        }
+    }
+    q.seq = ssu::uniform64(q.seq);
+    q.index = ssu::uniform64(q.index);
+    q.count = ssu::uniform64(q.count);
+    q.row = ssu::uniform64(q.row);
+    q.rows = __builtin_amdgcn_readfirstlane(q.rows);
+    return q;
+}
+
+// A thread's share of a tile's inputs, as loaded: x, z and dt of the rows that its wave
+// prepares, and elements of the tile's B and C.
+template <typename IT, typename DT, int ROWS, int ELEMENTS>
 struct Inputs {
-    typename Bits<IT>::type x[ROWS], z[ROWS];
-    unsigned dt[ROWS];
+    typename Bits<IT>::type x[ROWS], z[ROWS], bc[ELEMENTS];
+    typename Bits<DT>::type dt[ROWS];
 };
 
-// One pass over the pieces; OUT: the pass that writes outputs and final states.
-template <typename IT, int N, bool OUT>
-__global__ __launch_bounds__(64 * scan_waves(N)) void scan_kernel(const ScanParams p) {
-    constexpr int kWaves = scan_waves(N);
-    constexpr int NW = N / kWaves;            // state elements of a wave
-    constexpr int kOwn = kTile / kWaves;      // rows of a tile that a wave prepares and finishes
-    typedef Inputs<IT, kOwn> In;
-    __shared__ float4 vs[2][kTile / 2][64];                  // (v, v x) of two rows
-    __shared__ float4 ys[OUT ? kWaves : 1][OUT ? kTile / 4 : 1][64];  // partial y of four rows
+// What a pass over the pieces does: the first pass of prompts in pieces, or the pass that
+// writes outputs and final states, without or with the gate.
+enum Pass { kEnds, kPlain, kGated };
+
+// DT: dt's type, IT or float.
+template <typename IT, typename DT, int N, int PASS>
+__global__ __launch_bounds__(64 * scan_waves(N)) void scan_kernel(const ScanParams args) {
+    constexpr bool OUT = PASS != kEnds;
+    constexpr int kWaves = scan_waves(N), kThreads = 64 * kWaves;
+    constexpr int NW = N / kWaves;                 // state elements of a wave
+    constexpr int kOwn = kTile / kWaves;           // rows of a tile that a wave prepares and finishes
+    constexpr int kCells = kTile * 2 * N;          // elements of B and C of a tile
+    constexpr int kCopies = (kCells + kThreads - 1) / kThreads;
+    static_assert(kOwn >= 1 && kTile % kWaves == 0, "every wave has rows");
+    typedef Inputs<IT, DT, kOwn, kCopies> In;
+    typedef typename Bits<IT>::type bits;
+    typedef typename Bits<DT>::type dt_bits;
+    __shared__ float vs[2][2][kTile][64];                                 // v, and v x
+    __shared__ __align__(16) float bs[2][kTile][2 * N];                   // B, then C
+    __shared__ float ys[OUT ? 2 : 1][OUT ? kWaves : 1][OUT ? kTile : 1][64];  // partial y
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int blocks = p.blocks_per_group * p.ngroups;
-    const int64_t pi = blockIdx.x / blocks;
-    const int cb = blockIdx.x % blocks;
-    const Piece piece = p.table[pi];
+    const int blocks = args.blocks_per_group * args.ngroups;
+    const int item = args.piece ? blockIdx.x : fold(blockIdx.x, gridDim.x);
+    const int pi = item / blocks;
+    const int cb = item % blocks;
+    const Piece piece = find_piece(args, pi);
+    const scan_args& p = *fresh_args();
     if (piece.seq < 0 || (!OUT && piece.count == 1)) return;
     const int g = cb / p.blocks_per_group;
     const int in_group = (cb % p.blocks_per_group) * 64 + lane;
     const bool active = in_group < p.group_dim;
     const int c = g * p.group_dim + (active ? in_group : p.group_dim - 1);
     const int n0 = wave * NW;
-    const int64_t slot = scan_slot(p, piece.seq);
     const bool last = piece.index + 1 == piece.count;
     const bool has = p.has && p.has[piece.seq];
-    const int64_t at_state = slot * p.slot_stride + static_cast<int64_t>(c) * N + n0;
     const int64_t at_end = static_cast<int64_t>(c) * N + n0;
+    const int64_t at_state = scan_slot(p, piece.seq) * p.slot_stride + at_end;
     const int64_t ends_size = static_cast<int64_t>(p.dim) * N;
 
     float A[NW], s[NW];
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
-        A[i] = p.A[static_cast<int64_t>(c) * N + n0 + i] * kLog2e;
+        A[i] = p.A[at_end + i] * kLog2e;
         s[i] = 0.f;
     }
     if (!OUT && last) {
@@ -230,6 +268,7 @@ __global__ __launch_bounds__(64 * scan_waves(N)) void scan_kernel(const ScanPara
         }
     } else if (OUT) {
         // End state of piece 0 (which holds the entering state), then the others'.
+#pragma unroll NW <= 8 ? 4 : 1
         for (int64_t k = pi - piece.index; k < pi; ++k) {
             const float* from = p.ends + k * ends_size + at_end;
             const float sum = p.sums[k * p.dim + c];
@@ -241,107 +280,102 @@ __global__ __launch_bounds__(64 * scan_waves(N)) void scan_kernel(const ScanPara
 
     const float bias = p.dt_bias ? p.dt_bias[c] : 0.f;
     const float skip = OUT && p.D ? p.D[c] : 0.f;
-    const int64_t row0 = piece.row;
+    const bool softplus = p.softplus;
     const int rows = piece.rows;
 
-    // Rows are uniform over a wave: addresses are a scalar base and the lane's channel.
+    // This thread's elements of B and C in a tile: one column (of B, then of C), rows bc_row
+    // and every kThreads / 2 N-th after it.
+    static_assert(kThreads % (2 * N) == 0, "a thread stays in its column");
+    constexpr int kStep = kThreads / (2 * N);
+    const int bc_row = static_cast<int>(threadIdx.x) / (2 * N), bc_col = static_cast<int>(threadIdx.x) % (2 * N);
+    const int64_t bc_stride = bc_col < N ? p.B_stride : p.C_stride;
+    const bits* bc = static_cast<const bits*>(bc_col < N ? p.B : p.C) +
+                     (piece.row + bc_row) * bc_stride + g * N + bc_col % N;
+    // Requests this thread's share of the tile at row t0; each call is one tile on. Rows of x,
+    // z and dt are uniform over a wave: addresses are a scalar base and the lane's channel. Rows
+    // past the piece's end repeat its last one and are not used.
     const auto load = [&](int t0, In& in) {
 #pragma unroll
         for (int j = 0; j < kOwn; ++j) {
             const int t = t0 + wave * kOwn + j;
-            const int64_t row = row0 + (t < rows ? t : rows - 1);
-            typedef typename Bits<IT>::type bits;
-            in.x[j] = (reinterpret_cast<const bits*>(p.x) + row * p.x_stride)[c];
-            if (p.dt_f32)
-                in.dt[j] = (static_cast<const unsigned*>(p.dt) + row * p.dt_stride)[c];
-            else
-                in.dt[j] = (reinterpret_cast<const bits*>(p.dt) + row * p.dt_stride)[c];
-            if (OUT && p.z) in.z[j] = (reinterpret_cast<const bits*>(p.z) + row * p.z_stride)[c];
+            const int64_t row = piece.row + (t < rows ? t : rows - 1);
+            in.x[j] = (static_cast<const bits*>(p.x) + row * p.x_stride)[c];
+            in.dt[j] = (static_cast<const dt_bits*>(p.dt) + row * p.dt_stride)[c];
+            if (PASS == kGated) in.z[j] = (static_cast<const bits*>(p.z) + row * p.z_stride)[c];
         }
+#pragma unroll
+        for (int j = 0; j < kCopies; ++j)
+            if (bc_row + j * kStep < kTile && t0 + bc_row + j * kStep < rows)
+                in.bc[j] = bc[j * kStep * bc_stride];
+        bc += kTile * bc_stride;
     };
     float total = 0.f;  // sum of v over this wave's rows
-    const auto stage = [&](int t0, const In& in, int buf) {
-        float v[kOwn], vx[kOwn];
+    // Prepares this thread's share of a tile for all waves, and D x and the gate of its wave's
+    // rows for its own use at the tile's end.
+    const auto stage = [&](int t0, const In& in, int buf, float (&dx)[kOwn], float (&gate)[kOwn]) {
 #pragma unroll
         for (int j = 0; j < kOwn; ++j) {
-            float d = p.dt_f32 ? __uint_as_float(in.dt[j])
-                               : widen_io<IT>(static_cast<typename Bits<IT>::type>(in.dt[j]));
-            d += bias;
-            if (p.softplus) d = softplus_fast(d);
-            // Rows past the piece's end repeat its last one and are not used.
-            const bool in_piece = t0 + wave * kOwn + j < rows;
-            v[j] = d;
-            vx[j] = d * widen_io<IT>(in.x[j]);
-            if (!OUT && in_piece) total += d;
+            const int t = wave * kOwn + j;
+            const float d = widen_io<DT>(in.dt[j]) + bias;
+            const float v = softplus ? softplus_fast(d) : d;
+            const float x = widen_io<IT>(in.x[j]);
+            vs[buf][0][t][lane] = v;
+            vs[buf][1][t][lane] = v * x;
+            if (OUT) dx[j] = skip * x;
+            if (PASS == kGated) gate[j] = silu_fast(widen_io<IT>(in.z[j]));
+            if (!OUT && t0 + t < rows) total += v;
         }
 #pragma unroll
-        for (int j = 0; j < kOwn; j += 2)
-            vs[buf][(wave * kOwn + j) / 2][lane] = make_float4(v[j], vx[j], v[j + 1], vx[j + 1]);
+        for (int j = 0; j < kCopies; ++j)
+            if (bc_row + j * kStep < kTile)
+                bs[buf][bc_row + j * kStep][bc_col] = widen_io<IT>(in.bc[j]);
     };
 
-    In now, next;
-    load(0, now);
-    stage(0, now, 0);
-    if (kTile < rows) load(kTile, next);
+    In raw;
+    float dx[kOwn], gate[kOwn];
+    load(0, raw);
+    stage(0, raw, 0, dx, gate);
+    if (kTile < rows) load(kTile, raw);
     lds_barrier();
-    scalar_float* bc = (scalar_float*)(p.bc + ((row0 * p.ngroups + g) * kWaves + wave) * 2 * NW);
-    const int64_t bc_row = static_cast<int64_t>(p.ngroups) * kWaves * 2 * NW;
 
     for (int t0 = 0, buf = 0; t0 < rows; t0 += kTile, buf ^= 1) {
-        const bool more = t0 + kTile < rows;
-        if (more) stage(t0 + kTile, next, buf ^ 1);
-        const In mine = now;
-        now = next;
-        if (t0 + 2 * kTile < rows) load(t0 + 2 * kTile, next);
+        float next_dx[kOwn], next_gate[kOwn];
+        if (t0 + kTile < rows) stage(t0 + kTile, raw, buf ^ 1, next_dx, next_gate);
+        if (t0 + 2 * kTile < rows) load(t0 + 2 * kTile, raw);
 
-        // Four rows: `full` says at compile time that none lies past the piece's end.
-        const auto four = [&](int q, auto full) {
-            float y[4] = {0.f, 0.f, 0.f, 0.f};
-            const float4 p0 = vs[buf][2 * q][lane], p1 = vs[buf][2 * q + 1][lane];
-            const float v[4] = {p0.x, p0.z, p1.x, p1.z}, vx[4] = {p0.y, p0.w, p1.y, p1.w};
+        const auto row = [&](int t) {
+            const float v = vs[buf][0][t][lane], vx = vs[buf][1][t][lane];
+            float y = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = t0 + 4 * q + j;
-                if (!full.value && t >= rows) break;
-                scalar_float* b = bc + t * bc_row;
-#pragma unroll
-                for (int i = 0; i < NW; ++i) {
-                    const float e = __builtin_amdgcn_exp2f(v[j] * A[i]);
-                    s[i] = fmaf(e, s[i], vx[j] * b[i]);
-                    if constexpr (OUT) y[j] = fmaf(b[NW + i], s[i], y[j]);
-                }
+            for (int i = 0; i < NW; ++i) {
+                const float e = __builtin_amdgcn_exp2f(v * A[i]);
+                s[i] = fmaf(e, s[i], vx * bs[buf][t][n0 + i]);
+                if constexpr (OUT) y = fmaf(bs[buf][t][N + n0 + i], s[i], y);
             }
-            if constexpr (OUT) ys[wave][q][lane] = make_float4(y[0], y[1], y[2], y[3]);
+            if constexpr (OUT) ys[buf][wave][t][lane] = y;
         };
         if (t0 + kTile <= rows) {
-#pragma unroll 1
-            for (int q = 0; q < kTile / 4; ++q) four(q, std::true_type());
+#pragma unroll NW <= 8 ? kTile : NW <= 16 ? 2 : 1
+            for (int t = 0; t < kTile; ++t) row(t);
         } else {
 #pragma unroll 1
-            for (int q = 0; q < kTile / 4; ++q) four(q, std::false_type());
+            for (int t = 0; t0 + t < rows; ++t) row(t);
         }
         lds_barrier();
         if constexpr (OUT) {
-            // This wave's rows: the partial sums of each.
-            float y[kOwn];
-            const int q = wave * kOwn / 4, first = wave * kOwn % 4;
-#pragma unroll
-            for (int j = 0; j < kOwn; ++j) y[j] = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                const float* part = reinterpret_cast<const float*>(&ys[w][q][lane]) + first;
-#pragma unroll
-                for (int j = 0; j < kOwn; ++j) y[j] += part[j];
-            }
 #pragma unroll
             for (int j = 0; j < kOwn; ++j) {
-                const int t = t0 + wave * kOwn + j;
-                float v = fmaf(skip, widen_io<IT>(mine.x[j]), y[j]);
-                if (p.z) v *= silu_fast(widen_io<IT>(mine.z[j]));
-                if (t < rows && active)
-                    (static_cast<IT*>(p.out) + (row0 + t) * p.out_stride)[c] = static_cast<IT>(v);
+                const int t = wave * kOwn + j;
+                float y = dx[j];
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) y += ys[buf][w][t][lane];
+                if (PASS == kGated) y *= gate[j];
+                if (t0 + t < rows && active)
+                    (static_cast<IT*>(p.out) + (piece.row + t0 + t) * p.out_stride)[c] =
+                        static_cast<IT>(y);
+                dx[j] = next_dx[j];
+                gate[j] = next_gate[j];
             }
-            lds_barrier();
         }
     }
 
@@ -353,14 +387,14 @@ __global__ __launch_bounds__(64 * scan_waves(N)) void scan_kernel(const ScanPara
         if (active)
 #pragma unroll
             for (int i = 0; i < NW; ++i) p.ends[pi * ends_size + at_end + i] = s[i];
-        float* sums = reinterpret_cast<float*>(&vs[0][0][0]);
+        float* sums = &vs[0][0][0][0];
         sums[wave * 64 + lane] = total;
         lds_barrier();
         if (wave == 0 && active) {
             float all = 0.f;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) all += sums[w * 64 + lane];
-            p.sums[pi * p.dim + c] = all;
+            p.sums[static_cast<int64_t>(pi) * p.dim + c] = all;
         }
     }
 }
@@ -475,21 +509,19 @@ __host__ inline int step_channels(int64_t dstate, int64_t state_size) {
 
 // ---------------------------------------------------------------- the launchers
 
-template <typename IT>
-hipError_t launch_scan_varlen(const ScanParams& p, int dstate, hipStream_t stream) {
-    const int64_t cells = p.rows * p.ngroups * dstate;
-    const int64_t want = (cells + 4 * kPrepThreads - 1) / (4 * kPrepThreads);
-    const unsigned prep = static_cast<unsigned>(want < 1 ? 1 : want < 2048 ? want : 2048);
-    hipLaunchKernelGGL((scan_prepare_kernel<IT>), dim3(prep), dim3(kPrepThreads), 0, stream, p,
-                       dstate);
-    const int64_t grid64 = p.pieces * p.blocks_per_group * p.ngroups;
-    if (grid64 > INT32_MAX) return hipErrorInvalidConfiguration;
-    const dim3 grid(static_cast<unsigned>(grid64)), block(64 * scan_waves(dstate));
+template <typename IT, typename DT>
+hipError_t launch_scan_passes(const ScanParams& p, int dstate, hipStream_t stream) {
+    const int64_t blocks = p.pieces * p.blocks_per_group * p.ngroups;
+    if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
+    const dim3 grid(static_cast<unsigned>(blocks)), block(64 * scan_waves(dstate));
     const auto both = [&](auto n) {
         constexpr int N = decltype(n)::value;
-        if (p.piece < p.rows)
-            hipLaunchKernelGGL((scan_kernel<IT, N, false>), grid, block, 0, stream, p);
-        hipLaunchKernelGGL((scan_kernel<IT, N, true>), grid, block, 0, stream, p);
+        if (p.piece > 0)
+            hipLaunchKernelGGL((scan_kernel<IT, DT, N, kEnds>), grid, block, 0, stream, p);
+        if (p.z)
+            hipLaunchKernelGGL((scan_kernel<IT, DT, N, kGated>), grid, block, 0, stream, p);
+        else
+            hipLaunchKernelGGL((scan_kernel<IT, DT, N, kPlain>), grid, block, 0, stream, p);
     };
     switch (dstate) {
         case 8: both(std::integral_constant<int, 8>()); break;
@@ -501,6 +533,12 @@ hipError_t launch_scan_varlen(const ScanParams& p, int dstate, hipStream_t strea
         default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
+}
+
+template <typename IT>
+hipError_t launch_scan_varlen(const ScanParams& p, int dstate, hipStream_t stream) {
+    return p.dt_f32 ? launch_scan_passes<IT, float>(p, dstate, stream)
+                    : launch_scan_passes<IT, IT>(p, dstate, stream);
 }
 
 template <typename IT>

@@ -14,31 +14,28 @@ int64_t channel_blocks(int64_t dim, int64_t ngroups) {
     return (dim / ngroups + 63) / 64 * ngroups;
 }
 
-// Rows of a piece. With kEnough workgroups from the sequences alone nothing is cut.
-// Otherwise pieces are cut so that about kWanted come to be.
-constexpr int64_t kEnough = 512, kWanted = 1280, kShortest = 64;
+// Rows of a piece, or 0: with kEnough workgroups from the sequences alone, or none longer
+// than a piece, nothing is cut. Otherwise pieces are cut so that about kWanted come to be.
+constexpr int64_t kEnough = 512, kWanted = 1536, kShortest = 64;
 
 int64_t piece_rows(int64_t rows, int64_t nseq, int64_t blocks) {
-    if (nseq * blocks >= kEnough) return rows > 0 ? rows : 1;
+    if (nseq * blocks >= kEnough) return 0;
     const int64_t each = (rows * blocks + kWanted - 1) / kWanted;
     const int64_t piece = each < kShortest ? kShortest : each;
-    return (piece + kTile - 1) / kTile * kTile;
+    return piece < rows ? (piece + kTile - 1) / kTile * kTile : 0;
 }
 
 struct Scratch {
-    int64_t piece, pieces, table, bc, ends, sums, total;
+    int64_t piece, pieces, ends, sums, total;
 };
 
 Scratch scratch(int64_t rows, int64_t nseq, int64_t dim, int64_t dstate, int64_t ngroups) {
     Scratch s;
     s.piece = piece_rows(rows, nseq, channel_blocks(dim, ngroups));
-    s.pieces = rows / s.piece + nseq;
-    const bool cut = s.piece < rows;
-    s.table = 0;
-    s.bc = s.table + round_up(s.pieces * static_cast<int64_t>(sizeof(Piece)));
-    s.ends = s.bc + round_up(rows * ngroups * dstate * 2 * 4);
-    s.sums = s.ends + round_up(cut ? s.pieces * dim * dstate * 4 : 0);
-    s.total = s.sums + round_up(cut ? s.pieces * dim * 4 : 0);
+    s.pieces = s.piece > 0 ? rows / s.piece + nseq : nseq;
+    s.ends = 0;
+    s.sums = s.ends + round_up(s.piece > 0 ? s.pieces * dim * dstate * 4 : 0);
+    s.total = s.sums + round_up(s.piece > 0 ? s.pieces * dim * 4 : 0);
     return s;
 }
 
@@ -126,8 +123,8 @@ int check(const ssu_scan_args* a, bool varlen) {
     int64_t ws_bytes = 0;
     if (varlen) {
         ws_bytes = scratch(a->rows, a->nseq, a->dim, a->dstate, a->ngroups).total;
-        if (!a->workspace || !aligned(a->workspace, kAlign) ||
-            a->workspace_bytes < static_cast<size_t>(ws_bytes))
+        if (ws_bytes > 0 && (!a->workspace || !aligned(a->workspace, kAlign) ||
+                             a->workspace_bytes < static_cast<size_t>(ws_bytes)))
             return report(SSU_ERR_INVALID_ARGUMENT,
                           "workspace must be 256-byte aligned and hold %lld bytes (got %zu)",
                           (long long)ws_bytes, a->workspace_bytes);
@@ -208,8 +205,6 @@ int ssu_scan_varlen(const ssu_scan_args* a, void* stream) {
     char* ws = static_cast<char*>(a->workspace);
     p.piece = s.piece;
     p.pieces = s.pieces;
-    p.table = reinterpret_cast<Piece*>(ws + s.table);
-    p.bc = reinterpret_cast<float*>(ws + s.bc);
     p.ends = reinterpret_cast<float*>(ws + s.ends);
     p.sums = reinterpret_cast<float*>(ws + s.sums);
     p.blocks_per_group = (p.group_dim + 63) / 64;
