@@ -34,6 +34,10 @@ struct Raw {
         return *reinterpret_cast<const type*>(p);
     }
     static __device__ __forceinline__ void store(T* p, type v) { *reinterpret_cast<type*>(p) = v; }
+    // For results that the kernel does not read again.
+    static __device__ __forceinline__ void store_through(T* p, type v) {
+        __builtin_nontemporal_store(v, reinterpret_cast<type*>(p));
+    }
     static __device__ __forceinline__ void widen(type v, float (&f)[VEC]) {
         constexpr int per = ssu::Pack<T>::kPerWord;
 #pragma unroll
@@ -60,6 +64,10 @@ struct Raw<T, 1> {
         return *reinterpret_cast<const type*>(p);
     }
     static __device__ __forceinline__ void store(T* p, type v) { *reinterpret_cast<type*>(p) = v; }
+    // For results that the kernel does not read again.
+    static __device__ __forceinline__ void store_through(T* p, type v) {
+        __builtin_nontemporal_store(v, reinterpret_cast<type*>(p));
+    }
     static __device__ __forceinline__ void widen(type v, float (&f)[1]) {
         f[0] = ssu::widen_io<T>(v);
     }

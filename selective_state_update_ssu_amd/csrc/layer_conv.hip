@@ -180,7 +180,7 @@ __global__ __launch_bounds__(kThreads) void conv_varlen_kernel(const ConvParams 
             float now[VEC], y[VEC];
             R::widen(raw[j], now);
             taps<VEC, W>(w, bias, u, now, p.silu, y);
-            R::store(out + row * p.out_stride, R::narrow(y));
+            R::store_through(out + row * p.out_stride, R::narrow(y));
 #pragma unroll
             for (int k = 0; k + 1 < W - 1; ++k)
 #pragma unroll

@@ -402,8 +402,12 @@ __global__ __launch_bounds__(64 * scan_waves(N)) void scan_kernel(const ScanPara
 // ---------------------------------------------------------------- single tokens
 
 // Lanes share a channel's state row as 16-byte pieces: VEC elements per lane, LPR
-// lanes per channel, 64 / LPR channels per wave instruction, kLoads of them in
-// flight. A wave's channels lie in one group, so it reads B and C once.
+// lanes per channel, 64 / LPR channels per wave instruction, LOADS of them in flight. A
+// wave's channels lie in one group, so it reads B and C once. The state's bytes bound it:
+// 512 sequences of 5,120 x 16 in fp32 (356 MB) take 67 us on states that no cache holds,
+// 5.3 TB/s (a copy streams at 5.4); 76 us with loads and stores that the caches keep. One
+// and four loads in flight take 69 and 67 us, rows of the same channels one after the
+// other, which reads A once, 67 to 71 us.
 template <typename ST, int N>
 struct StepShape {
     static constexpr int VEC = 16 / static_cast<int>(sizeof(ST));
@@ -411,92 +415,118 @@ struct StepShape {
     static constexpr int RPI = 64 / LPR;  // channels per instruction
 };
 
-// VEC elements of B or C at p.
-template <typename IT, int VEC>
-__device__ __forceinline__ void load_elements(const IT* p, bool wide, float (&f)[VEC]) {
-    constexpr int kPiece = VEC * static_cast<int>(sizeof(IT)) > 16 ? 4 : VEC;
-    if (wide) {
+// VEC elements of B or C, as loaded: in 16-byte pieces (or one shorter one) where alignment
+// allows (WIDE), else one by one.
+template <typename IT, int VEC, bool WIDE>
+struct Elements {
+    static constexpr int kPiece = !WIDE ? 1 : VEC * static_cast<int>(sizeof(IT)) > 16 ? 4 : VEC;
+    typename Raw<IT, kPiece>::type raw[VEC / kPiece];
+    __device__ __forceinline__ void load(const void* base, int64_t at) {
+        const IT* p = static_cast<const IT*>(base) + at;
 #pragma unroll
-        for (int k = 0; k < VEC; k += kPiece) {
-            float h[kPiece];
-            Raw<IT, kPiece>::widen(Raw<IT, kPiece>::load(p + k), h);
-#pragma unroll
-            for (int i = 0; i < kPiece; ++i) f[k + i] = h[i];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) f[i] = static_cast<float>(p[i]);
+        for (int k = 0; k < VEC / kPiece; ++k) raw[k] = Raw<IT, kPiece>::load(p + k * kPiece);
     }
-}
+    __device__ __forceinline__ void widen(float (&f)[VEC]) const {
+#pragma unroll
+        for (int k = 0; k < VEC / kPiece; ++k) {
+            float h[kPiece];
+            Raw<IT, kPiece>::widen(raw[k], h);
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) f[k * kPiece + i] = h[i];
+        }
+    }
+};
 
-template <typename ST, typename IT, int N, int LOADS>
+// A load under a condition, or its conversion between two loads, would be waited for on the
+// spot: all loads of a row are unconditional (an absent z or D is read as x or A and not
+// used) and precede every use.
+template <typename ST, typename IT, typename DT, int N, int LOADS, bool WIDE>
 __global__ __launch_bounds__(256) void scan_update_kernel(const ScanParams p) {
     typedef StepShape<ST, N> Shape;
     constexpr int VEC = Shape::VEC, LPR = Shape::LPR, RPI = Shape::RPI;
     constexpr int W = VEC / Pack<ST>::kPerWord;
     typedef typename Words<W>::type words_t;
+    typedef typename Bits<IT>::type bits;
+    typedef typename Bits<DT>::type dt_bits;
     const int lane = threadIdx.x & 63;
     const int sub = lane % LPR;
-    const int64_t wave = static_cast<int64_t>(blockIdx.x) * 4 +
+    const int64_t wave = ssu::xcd_tile(blockIdx.x, gridDim.x) * 4 +
                          __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int blocks = p.blocks_per_group * p.ngroups;
     const int64_t b = wave / blocks;
     if (b >= p.rows) return;
-    const int cb = static_cast<int>(wave % blocks);
     const int64_t slot = scan_slot(p, b);
     if (slot < 0) return;
+    const int cb = static_cast<int>(wave % blocks);
     const int g = cb / p.blocks_per_group;
     const int first = (cb % p.blocks_per_group) * (RPI * LOADS) + lane / LPR;  // in the group
+    const bits* gate = static_cast<const bits*>(p.z ? p.z : p.x);
+    const int64_t gate_stride = p.z ? p.z_stride : p.x_stride;
 
-    words_t raw[LOADS];
-    float x[LOADS], d[LOADS], z[LOADS];
-    ST* state = static_cast<ST*>(p.state) + slot * p.slot_stride + sub * VEC;
+    // Lanes past the group repeat its last channel and store nothing.
+    int c[LOADS];
+    bool active[LOADS];
+    float A[LOADS][VEC], D[LOADS], bias[LOADS];
 #pragma unroll
     for (int k = 0; k < LOADS; ++k) {
         const int in_group = first + k * RPI;
-        if (in_group >= p.group_dim) continue;
-        const int c = g * p.group_dim + in_group;
-        raw[k] = __builtin_nontemporal_load(
-            reinterpret_cast<const words_t*>(state + static_cast<int64_t>(c) * N));
-        x[k] = static_cast<float>((static_cast<const IT*>(p.x) + b * p.x_stride)[c]);
-        d[k] = p.dt_f32 ? (static_cast<const float*>(p.dt) + b * p.dt_stride)[c]
-                        : static_cast<float>((static_cast<const IT*>(p.dt) + b * p.dt_stride)[c]);
-        if (p.z) z[k] = static_cast<float>((static_cast<const IT*>(p.z) + b * p.z_stride)[c]);
+        active[k] = in_group < p.group_dim;
+        c[k] = g * p.group_dim + (active[k] ? in_group : p.group_dim - 1);
+        D[k] = (p.D ? p.D : p.A)[c[k]];
+        bias[k] = (p.dt_bias ? p.dt_bias : p.A)[c[k]];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) A[k][i] = p.A[static_cast<int64_t>(c[k]) * N + sub * VEC + i];
     }
-    float B[VEC], C[VEC];
-    load_elements<IT, VEC>(static_cast<const IT*>(p.B) + b * p.B_stride + g * N + sub * VEC,
-                           p.wide_bc, B);
-    load_elements<IT, VEC>(static_cast<const IT*>(p.C) + b * p.C_stride + g * N + sub * VEC,
-                           p.wide_bc, C);
+
+    ST* state = static_cast<ST*>(p.state) + slot * p.slot_stride + sub * VEC;
+    words_t raw[LOADS];
+    bits x_in[LOADS], z_in[LOADS];
+    dt_bits dt_in[LOADS];
+    Elements<IT, VEC, WIDE> B_in, C_in;
+#pragma unroll
+    for (int k = 0; k < LOADS; ++k)
+        raw[k] = __builtin_nontemporal_load(
+            reinterpret_cast<const words_t*>(state + static_cast<int64_t>(c[k]) * N));
 #pragma unroll
     for (int k = 0; k < LOADS; ++k) {
-        const int in_group = first + k * RPI;
-        // The lanes of a channel agree here, so its sum has all of them.
-        if (in_group >= p.group_dim) continue;
-        const int c = g * p.group_dim + in_group;
-        float v = d[k] + (p.dt_bias ? p.dt_bias[c] : 0.f);
-        if (p.softplus) v = softplus_fast(v);
-        const float vx = v * x[k];
-        const float* A = p.A + static_cast<int64_t>(c) * N + sub * VEC;
-        float s[VEC], y = 0.f;
+        dt_in[k] = (static_cast<const dt_bits*>(p.dt) + b * p.dt_stride)[c[k]];
+        x_in[k] = (static_cast<const bits*>(p.x) + b * p.x_stride)[c[k]];
+        z_in[k] = (gate + b * gate_stride)[c[k]];
+    }
+    B_in.load(p.B, b * p.B_stride + g * N + sub * VEC);
+    C_in.load(p.C, b * p.C_stride + g * N + sub * VEC);
+    float B[VEC], C[VEC];
+    B_in.widen(B);
+    C_in.widen(C);
+    // Stores after all arithmetic: a load's arrival is counted together with earlier stores.
+    float y[LOADS];
+#pragma unroll
+    for (int k = 0; k < LOADS; ++k) {
+        const float x = widen_io<IT>(x_in[k]);
+        const float d = widen_io<DT>(dt_in[k]) + (p.dt_bias ? bias[k] : 0.f);
+        const float v = p.softplus ? softplus_fast(d) : d;
+        const float vx = v * x, vl = v * kLog2e;
+        float s[VEC], sum = 0.f;
 #pragma unroll
         for (int i = 0; i < W; ++i) Pack<ST>::widen(raw[k][i], &s[i * Pack<ST>::kPerWord]);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            const float e = __builtin_amdgcn_exp2f(v * (A[i] * kLog2e));
+            const float e = __builtin_amdgcn_exp2f(vl * A[k][i]);
             s[i] = fmaf(e, s[i], vx * B[i]);
-            y = fmaf(C[i], s[i], y);
+            sum = fmaf(C[i], s[i], sum);
         }
 #pragma unroll
         for (int i = 0; i < W; ++i) raw[k][i] = Pack<ST>::narrow(&s[i * Pack<ST>::kPerWord]);
-        __builtin_nontemporal_store(raw[k],
-                                    reinterpret_cast<words_t*>(state + static_cast<int64_t>(c) * N));
-        if constexpr (LPR > 1) y = group_sum<LPR>(y);
-        if (sub == 0) {
-            if (p.D) y = fmaf(p.D[c], x[k], y);
-            if (p.z) y *= silu_fast(z[k]);
-            (static_cast<IT*>(p.out) + b * p.out_stride)[c] = static_cast<IT>(y);
-        }
+        if constexpr (LPR > 1) sum = group_sum<LPR>(sum);
+        sum = fmaf(p.D ? D[k] : 0.f, x, sum);
+        y[k] = sum * (p.z ? silu_fast(widen_io<IT>(z_in[k])) : 1.f);
+    }
+#pragma unroll
+    for (int k = 0; k < LOADS; ++k) {
+        if (!active[k]) continue;
+        __builtin_nontemporal_store(
+            raw[k], reinterpret_cast<words_t*>(state + static_cast<int64_t>(c[k]) * N));
+        if (sub == 0) (static_cast<IT*>(p.out) + b * p.out_stride)[c[k]] = static_cast<IT>(y[k]);
     }
 }
 
@@ -541,19 +571,19 @@ hipError_t launch_scan_varlen(const ScanParams& p, int dstate, hipStream_t strea
                     : launch_scan_passes<IT, IT>(p, dstate, stream);
 }
 
-template <typename IT>
-hipError_t launch_scan_update(const ScanParams& p, int dstate, hipStream_t stream) {
+template <typename IT, typename DT, bool WIDE>
+hipError_t launch_scan_step(const ScanParams& p, int dstate, hipStream_t stream) {
     const int64_t waves = p.rows * p.blocks_per_group * p.ngroups;
     if ((waves + 3) / 4 > INT32_MAX) return hipErrorInvalidConfiguration;
     const dim3 grid(static_cast<unsigned>((waves + 3) / 4)), block(256);
     const auto go = [&](auto n) {
-        constexpr int N = decltype(n)::value;
+        constexpr int N = decltype(n)::value, L = kStepLoads;
         if (p.state_dtype == SSU_F32)
-            hipLaunchKernelGGL((scan_update_kernel<float, IT, N, kStepLoads>), grid, block, 0, stream, p);
+            hipLaunchKernelGGL((scan_update_kernel<float, IT, DT, N, L, WIDE>), grid, block, 0, stream, p);
         else if (p.state_dtype == SSU_F16)
-            hipLaunchKernelGGL((scan_update_kernel<_Float16, IT, N, kStepLoads>), grid, block, 0, stream, p);
+            hipLaunchKernelGGL((scan_update_kernel<_Float16, IT, DT, N, L, WIDE>), grid, block, 0, stream, p);
         else
-            hipLaunchKernelGGL((scan_update_kernel<__bf16, IT, N, kStepLoads>), grid, block, 0, stream, p);
+            hipLaunchKernelGGL((scan_update_kernel<__bf16, IT, DT, N, L, WIDE>), grid, block, 0, stream, p);
     };
     switch (dstate) {
         case 8: go(std::integral_constant<int, 8>()); break;
@@ -565,6 +595,15 @@ hipError_t launch_scan_update(const ScanParams& p, int dstate, hipStream_t strea
         default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
+}
+
+template <typename IT>
+hipError_t launch_scan_update(const ScanParams& p, int dstate, hipStream_t stream) {
+    if (p.dt_f32)
+        return p.wide_bc ? launch_scan_step<IT, float, true>(p, dstate, stream)
+                         : launch_scan_step<IT, float, false>(p, dstate, stream);
+    return p.wide_bc ? launch_scan_step<IT, IT, true>(p, dstate, stream)
+                     : launch_scan_step<IT, IT, false>(p, dstate, stream);
 }
 
 // One per io dtype, each in its own translation unit.
