@@ -23,7 +23,12 @@ LIBRARY = os.path.join(LIB_DIR, "libssu_amd.so")
 STREAM_LIBRARY = os.path.join(LIB_DIR, "libssu_stream.so")
 STREAM_SOURCES = ["stream_ceiling.hip"]
 
+# Python side of include/layer.h: host code against torch's headers, linked to the library.
+BINDING = os.path.join(LIB_DIR, "_layer_binding.so")
+BINDING_SOURCE = "layer_binding.cpp"
+
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("HIP_CXX", "/opt/rocm/llvm/bin/clang++")
 ARCH = "gfx950"
 SOURCES = ["ssu_api.hip", "ssu_kernels_f32.hip", "ssu_kernels_f16.hip", "ssu_kernels_bf16.hip",
            "ring_trackers.hip", "ssd_api.hip", "ssd_kernels_bf16.hip", "ssd_kernels_f16.hip",
@@ -54,6 +59,17 @@ def _run(cmd):
     return msg
 
 
+def _binding_flags():
+    import sysconfig
+
+    import torch
+    import torch.utils.cpp_extension as ext
+    include = ext.include_paths() + [sysconfig.get_paths()["include"], "/opt/rocm/include"]
+    return ["-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            f"-I{INCLUDE}", *[f"-isystem{p}" for p in include]]
+
+
 def build(verbose: bool = False) -> str:
     """Compile every source and link the library; returns its path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -61,20 +77,30 @@ def build(verbose: bool = False) -> str:
 
     def compile_one(src):
         obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-        msg = _run([HIPCC, *CXXFLAGS, "-c", os.path.join(CSRC, src), "-o", obj])
-        return obj, msg
+        if src == BINDING_SOURCE:
+            cmd = [CXX, *_binding_flags()]
+        else:
+            cmd = [HIPCC, *CXXFLAGS]
+        return obj, _run([*cmd, "-c", os.path.join(CSRC, src), "-o", obj])
 
-    with ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 1)) as ex:
-        results = list(ex.map(compile_one, SOURCES + STREAM_SOURCES))
+    sources = SOURCES + STREAM_SOURCES + [BINDING_SOURCE]
+    with ThreadPoolExecutor(max_workers=min(len(sources), os.cpu_count() or 1)) as ex:
+        results = list(ex.map(compile_one, sources))
     for obj, msg in results:
         if msg and verbose:
             print(msg, file=sys.stderr)
-    objs = dict(zip(SOURCES + STREAM_SOURCES, (o for o, _ in results)))
+    objs = dict(zip(sources, (o for o, _ in results)))
     for lib, srcs in ((LIBRARY, SOURCES), (STREAM_LIBRARY, STREAM_SOURCES)):
         tmp = lib + ".tmp"
         _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp,
               *[objs[s] for s in srcs]])
         os.replace(tmp, lib)
+    import torch
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    _run([CXX, "-shared", "-fPIC", "-o", BINDING + ".tmp", objs[BINDING_SOURCE],
+          f"-L{LIB_DIR}", "-l:" + os.path.basename(LIBRARY), "-Wl,-rpath,$ORIGIN", f"-L{torch_lib}", "-ltorch_python", "-ltorch_cpu", "-lc10",
+          "-lc10_hip"])
+    os.replace(BINDING + ".tmp", BINDING)
     return LIBRARY
 
 
