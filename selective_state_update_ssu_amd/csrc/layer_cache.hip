@@ -116,21 +116,24 @@ constexpr int kThreads = 256;
 constexpr int kDepth = 4;                              // loads in flight per lane and pair
 constexpr int kPairs = 4;                              // neighbouring pairs of a workgroup
 constexpr int64_t kTile = kThreads * kDepth * 16;      // bytes of a slot per workgroup
+constexpr int64_t kMostItems = INT32_MAX / 2;          // (tile, group) pairs of one launch
 constexpr int kMaxCaches = 32;                         // caches of one launch
 
 struct Block {
     char* base;
     int64_t slot_bytes, stride;
-    int64_t first_tile;
 };
 
 struct CopyParams {
     const void* src;
     const void* dst;
     const int32_t* plan;  // compaction: moves in plan_kernel's layout, else NULL
-    int64_t n, nslots, half, tiles;
+    int64_t first, n;     // pairs of this launch (of a plan's: at most)
+    int64_t nslots, half;
+    int32_t tiles;        // of a slot in all caches
     int32_t src64, dst64, ncaches;
     uint32_t wide;        // bit i: cache[i] moves 16 bytes at a time
+    int32_t first_tile[kMaxCaches];
     Block cache[kMaxCaches];
 };
 
@@ -139,8 +142,8 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 // One tile of one slot (bytes [at, at + kTile) of it, cut at its end): the four
 // 16-byte pieces of a lane, or where a cache's slots are not 16-byte aligned its
 // bytes one by one.
-__device__ __forceinline__ void copy_tile(const Block& c, int64_t at, const int64_t (&from)[kPairs],
-                                          const int64_t (&to)[kPairs], bool wide) {
+__device__ __forceinline__ void copy_tile(const Block& c, int64_t at, const int (&from)[kPairs],
+                                          const int (&to)[kPairs], bool wide) {
     if (wide) {
         u32x4 v[kPairs][kDepth];
 #pragma unroll
@@ -186,29 +189,35 @@ __device__ __forceinline__ void copy_tile(const Block& c, int64_t at, const int6
 // stores take 510 us there and 145 instead of 136 us on 36 moves of 10.6 MB; kept are those
 // that leave the caches to others. (A copy streams at 5.4 TB/s, a fill at 5.6.)
 __global__ __launch_bounds__(kThreads) void copy_kernel(const CopyParams p) {
-    const int64_t n = p.plan ? p.plan[0] : p.n;
-    const int64_t items = (n + kPairs - 1) / kPairs * p.tiles;
-    for (int64_t k = blockIdx.x; k < items; k += gridDim.x) {
-        const int64_t item = ssu::xcd_tile(k, items);
-        const int64_t group = item / p.tiles, tile = item % p.tiles;
-        int ci = 0;
-        while (ci + 1 < p.ncaches && tile >= p.cache[ci + 1].first_tile) ++ci;
+    const int lane = threadIdx.x & 63;
+    int64_t n = p.n;
+    if (p.plan) n = p.plan[0] - p.first < n ? p.plan[0] - p.first : n;
+    const int first_tile = lane < p.ncaches ? p.first_tile[lane] : 0x7fffffff;
+    const int items = static_cast<int>((n + kPairs - 1) / kPairs) * p.tiles;
+    for (int k = blockIdx.x; k < items; k += gridDim.x) {
+        const int item = static_cast<int>(ssu::xcd_tile(k, items));
+        const int group = item / p.tiles, tile = item % p.tiles;
+        const int ci = __builtin_popcountll(__ballot(first_tile <= tile)) - 1;
         const Block c = p.cache[ci];
-        int64_t from[kPairs], to[kPairs];
-#pragma unroll
-        for (int k = 0; k < kPairs; ++k) {
-            const int64_t i = group * kPairs + k;
-            from[k] = to[k] = -1;
-            if (i < n) {
-                const int64_t s = p.plan ? p.plan[1 + i] : load_index(p.src, p.src64, i);
-                const int64_t d = p.plan ? p.plan[1 + p.half + i] : load_index(p.dst, p.dst64, i);
-                if (s >= 0 && s < p.nslots && d >= 0 && d < p.nslots && s != d) {
-                    from[k] = s;
-                    to[k] = d;
-                }
+        const int64_t in_slot = static_cast<int64_t>(tile - __builtin_amdgcn_readlane(first_tile, ci)) * kTile;
+        // Lane k < kPairs reads pair k's ids: one wait for all of them.
+        const int64_t mine = static_cast<int64_t>(group) * kPairs + lane, at = p.first + mine;
+        int from_lane = -1, to_lane = -1;
+        if (lane < kPairs && mine < n) {
+            const int64_t s = p.plan ? p.plan[1 + at] : load_index(p.src, p.src64, at);
+            const int64_t d = p.plan ? p.plan[1 + p.half + at] : load_index(p.dst, p.dst64, at);
+            if (s >= 0 && s < p.nslots && d >= 0 && d < p.nslots && s != d) {
+                from_lane = static_cast<int>(s);
+                to_lane = static_cast<int>(d);
             }
         }
-        copy_tile(c, (tile - c.first_tile) * kTile, from, to, p.wide >> ci & 1);
+        int from[kPairs], to[kPairs];
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) {
+            from[k] = __builtin_amdgcn_readlane(from_lane, k);
+            to[k] = __builtin_amdgcn_readlane(to_lane, k);
+        }
+        copy_tile(c, in_slot, from, to, p.wide >> ci & 1);
     }
 }
 
@@ -274,31 +283,39 @@ int copy(const ssu_cache_args* a, const int32_t* plan, const void* src, int src6
         p.src64 = src64;
         p.dst64 = dst64;
         p.plan = plan;
-        p.n = n;
         p.nslots = a->nslots;
         p.half = a->nslots / 2;
         while (done < a->ncaches && p.ncaches < kMaxCaches) {
-            const ssu_cache_block& c = a->caches[done++];
-            if (c.slot_bytes == 0) continue;
-            Block& b = p.cache[p.ncaches];
-            b.base = static_cast<char*>(c.base);
-            b.slot_bytes = c.slot_bytes;
-            b.stride = c.stride_bytes;
-            b.first_tile = p.tiles;
-            p.tiles += (c.slot_bytes + kTile - 1) / kTile;
+            const ssu_cache_block& c = a->caches[done];
+            const int64_t tiles = (c.slot_bytes + kTile - 1) / kTile;
+            if (tiles > kMostItems - p.tiles) {
+                if (p.ncaches == 0)
+                    return ssu::report(SSU_ERR_UNSUPPORTED, "%s: a slot of %lld bytes is too large",
+                                       entry, (long long)c.slot_bytes);
+                break;
+            }
+            ++done;
+            if (tiles == 0) continue;
+            p.cache[p.ncaches] = {static_cast<char*>(c.base), c.slot_bytes, c.stride_bytes};
+            p.first_tile[p.ncaches] = p.tiles;
+            p.tiles += static_cast<int32_t>(tiles);
             if (aligned(c.base, 16) && c.slot_bytes % 16 == 0 && c.stride_bytes % 16 == 0)
                 p.wide |= 1u << p.ncaches;
             ++p.ncaches;
         }
         if (p.ncaches == 0) continue;
-        const int64_t items = (n + kPairs - 1) / kPairs * p.tiles;
-        // One item per workgroup, but for compactions, whose moves are known on the device
-        // only and may be few: there the grid is bounded.
-        const int64_t most = plan ? 65536 : INT32_MAX;
-        const int64_t grid = items < most ? items : most;
-        hipLaunchKernelGGL(copy_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream,
-                           p);
-        if (int rc = launched(entry)) return rc;
+        // The kernel counts its items in 32 bits.
+        const int64_t most = kMostItems / p.tiles * kPairs;
+        for (p.first = 0; p.first < n; p.first += most) {
+            p.n = n - p.first < most ? n - p.first : most;
+            const int64_t items = (p.n + kPairs - 1) / kPairs * p.tiles;
+            // One item per workgroup, but for compactions, whose moves are known on the
+            // device only and may be few: there the grid is bounded.
+            const int64_t grid = plan && items > 65536 ? 65536 : items;
+            hipLaunchKernelGGL(copy_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
+                               stream, p);
+            if (int rc = launched(entry)) return rc;
+        }
     }
     return ssu::report_ok();
 }

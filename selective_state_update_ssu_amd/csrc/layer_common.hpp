@@ -34,7 +34,10 @@ struct Raw {
         return *reinterpret_cast<const type*>(p);
     }
     static __device__ __forceinline__ void store(T* p, type v) { *reinterpret_cast<type*>(p) = v; }
-    // For results that the kernel does not read again.
+    // Past the caches: for what is not read again before much else is.
+    static __device__ __forceinline__ type load_through(const T* p) {
+        return __builtin_nontemporal_load(reinterpret_cast<const type*>(p));
+    }
     static __device__ __forceinline__ void store_through(T* p, type v) {
         __builtin_nontemporal_store(v, reinterpret_cast<type*>(p));
     }
@@ -64,7 +67,10 @@ struct Raw<T, 1> {
         return *reinterpret_cast<const type*>(p);
     }
     static __device__ __forceinline__ void store(T* p, type v) { *reinterpret_cast<type*>(p) = v; }
-    // For results that the kernel does not read again.
+    // Past the caches: for what is not read again before much else is.
+    static __device__ __forceinline__ type load_through(const T* p) {
+        return __builtin_nontemporal_load(reinterpret_cast<const type*>(p));
+    }
     static __device__ __forceinline__ void store_through(T* p, type v) {
         __builtin_nontemporal_store(v, reinterpret_cast<type*>(p));
     }

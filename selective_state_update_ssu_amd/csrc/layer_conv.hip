@@ -27,7 +27,7 @@ struct ConvParams {
     int64_t nslots, slot_stride, x_stride, out_stride, rows, dim, nseq, pad_slot_id;
     int64_t waves;          // (tile, channel block) pairs
     int32_t channel_blocks;
-    int32_t tile;           // rows of a wave
+    int32_t tile;           // rows of a wave, at least 3 for packed prompts
     int32_t cu64, slot64, silu;
 };
 
@@ -46,37 +46,90 @@ __device__ __forceinline__ void taps(const float (&w)[W][VEC], const float (&bia
     }
 }
 
-// The lane's taps (weight is [dim, width]: VEC * W adjacent elements) and bias.
+// The lane's taps (weight is [dim, width]: VEC * W adjacent elements) and bias: requested
+// first, widened once other requests are on their way.
 template <typename T, int VEC, int W>
-__device__ __forceinline__ void load_taps(const ConvParams& p, int64_t c0, float (&w)[W][VEC],
-                                          float (&bias)[VEC]) {
-    const T* src = static_cast<const T*>(p.weight) + c0 * W;
+struct Taps {
+    typename Raw<T, VEC>::type raw[W], raw_bias;
+    __device__ __forceinline__ void request(const ConvParams& p, int64_t c0) {
+        const T* src = static_cast<const T*>(p.weight) + c0 * W;
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-        float f[VEC];
-        Raw<T, VEC>::widen(Raw<T, VEC>::load(src + k * VEC), f);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) w[(k * VEC + i) % W][(k * VEC + i) / W] = f[i];
+        for (int k = 0; k < W; ++k) raw[k] = Raw<T, VEC>::load(src + k * VEC);
+        // Without a bias the taps' first elements are read and not used.
+        raw_bias = Raw<T, VEC>::load(p.bias ? static_cast<const T*>(p.bias) + c0 : src);
     }
-    if (p.bias) {
-        Raw<T, VEC>::widen(Raw<T, VEC>::load(static_cast<const T*>(p.bias) + c0), bias);
-    } else {
+    __device__ __forceinline__ void widen(const ConvParams& p, float (&w)[W][VEC],
+                                          float (&bias)[VEC]) const {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) bias[i] = 0.f;
+        for (int k = 0; k < W; ++k) {
+            float f[VEC];
+            Raw<T, VEC>::widen(raw[k], f);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[(k * VEC + i) % W][(k * VEC + i) / W] = f[i];
+        }
+        Raw<T, VEC>::widen(raw_bias, bias);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) bias[i] = p.bias ? bias[i] : 0.f;
     }
-}
+};
 
 __device__ __forceinline__ int64_t slot_of(const ConvParams& p, int64_t b) {
     const int64_t s = p.slots ? load_index(p.slots, p.slot64, b) : b;
     return s != p.pad_slot_id && s >= 0 && s < p.nslots ? s : -1;
 }
 
+// The sequences of a call as a wave sees them. Up to 63 are read at once, a lane each, and
+// handed over between lanes: what a short call waits for are dependent reads.
+struct Sequences {
+    const ConvParams& p;
+    int64_t start, slot;  // this lane's sequence: its first row, its slot or -1
+    int has;
+    bool few;
+    __device__ __forceinline__ explicit Sequences(const ConvParams& params) : p(params) {
+        const int lane = threadIdx.x & 63;
+        few = p.nseq < 64;
+        start = slot = has = 0;
+        if (few && lane <= p.nseq) {
+            start = load_index(p.cu, p.cu64, lane);
+            if (lane < p.nseq) {
+                slot = slot_of(p, lane);
+                has = p.has && p.has[lane];
+            }
+        }
+    }
+    static __device__ __forceinline__ int64_t lane64(int64_t v, int64_t i) {
+        const unsigned lo = __builtin_amdgcn_readlane(static_cast<unsigned>(v), static_cast<int>(i));
+        const unsigned hi = __builtin_amdgcn_readlane(static_cast<unsigned>(v >> 32), static_cast<int>(i));
+        return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+    }
+    // The last sequence that starts at or before `row`, or -1.
+    __device__ __forceinline__ int64_t at(int64_t row) const {
+        if (!few) return ssu::uniform64(count_starts(p.cu, p.cu64, p.nseq, row) - 1);
+        const bool in = static_cast<int>(threadIdx.x & 63) < p.nseq && start <= row;
+        return __builtin_popcountll(__ballot(in)) - 1;
+    }
+    __device__ __forceinline__ int64_t begin(int64_t i) const {
+        return few ? lane64(start, i) : ssu::uniform64(load_index(p.cu, p.cu64, i));
+    }
+    __device__ __forceinline__ int64_t slot_at(int64_t i) const {
+        return few ? lane64(slot, i) : ssu::uniform64(slot_of(p, i));
+    }
+    __device__ __forceinline__ bool has_at(int64_t i) const {
+        return few ? __builtin_amdgcn_readlane(has, static_cast<int>(i)) : p.has && p.has[i];
+    }
+};
+
 // Packed prompts. A wave walks `tile` packed rows of one channel block. Where a
 // sequence starts it takes the slot's history, and it stores the sequence's final
 // history too, so no other wave touches that slot: a wave whose tile begins
 // within the first width - 1 rows of a sequence leaves those to the wave before
 // it, which goes on past its own tile for them. Inputs are requested kBatch rows
-// ahead of their use.
+// ahead of their use, the first ones before the rows' sequences are known.
+//
+// Memory bounds long prompts: 17,885 rows of 10,240 channels in bf16 (733 MB) take 134 us, 5.5
+// TB/s, with tiles of 16 rows (150, 153 and 162 us with 8, 32 and 64) and outputs that
+// bypass the caches (146 us without; 149 us if the inputs bypass them too). Few rows are
+// latency: tiles of 4 rows then put more waves on it.
 template <typename T, int VEC, int W>
 __global__ __launch_bounds__(kThreads) void conv_varlen_kernel(const ConvParams p) {
     constexpr int kBatch = 8;
@@ -89,15 +142,37 @@ __global__ __launch_bounds__(kThreads) void conv_varlen_kernel(const ConvParams 
     const int64_t r0 = wave / p.channel_blocks * p.tile;
     const int64_t r1 = r0 + p.tile < p.rows ? r0 + p.tile : p.rows;
 
+    // Lanes past the last channel repeat the first and store nothing: the whole wave stays
+    // together, since its lanes hold the sequences.
+    const bool inside = c0 < p.dim;
+    const int64_t c = inside ? c0 : 0;
+    const T* x = static_cast<const T*>(p.x) + c;
+    typename R::type raw[kBatch], before[W - 1];
+    const auto request = [&](int64_t from, int64_t last) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            raw[j] = R::load(x + (from + j < last ? from + j : last - 1) * p.x_stride);
+    };
+    const auto request_before = [&](int64_t row) {
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+            const int64_t q = row - (W - 1) + k;
+            before[k] = R::load(x + (q > 0 ? q : 0) * p.x_stride);
+        }
+    };
+    const Sequences seqs(p);
+    Taps<T, VEC, W> taps_in;
+    taps_in.request(p, c);
+    request_before(r0);
+    request(r0, p.rows);
+
     // The sequence of row r0, and the rows that are this wave's.
-    int64_t b = count_starts(p.cu, p.cu64, p.nseq, r0) - 1;
-    b = ssu::uniform64(b);
-    int64_t begin = 0, end = 0, slot = -1;
+    int64_t b = seqs.at(r0), begin = 0, end = 0, slot = -1;
     const auto enter = [&](int64_t i) {
         b = i;
-        begin = load_index(p.cu, p.cu64, i);
-        end = load_index(p.cu, p.cu64, i + 1);
-        slot = begin >= 0 && begin <= end && end <= p.rows ? slot_of(p, i) : -1;
+        begin = seqs.begin(i);
+        end = seqs.begin(i + 1);
+        slot = begin >= 0 && begin <= end && end <= p.rows ? seqs.slot_at(i) : -1;
     };
     int64_t r = r0, stop = r1;
     if (b >= 0) {
@@ -108,43 +183,33 @@ __global__ __launch_bounds__(kThreads) void conv_varlen_kernel(const ConvParams 
         int64_t lb = begin, le = end;
         bool ok = slot >= 0;
         if (!(b >= 0 && r1 <= le)) {
-            const int64_t last = ssu::uniform64(count_starts(p.cu, p.cu64, p.nseq, r1 - 1) - 1);
-            if (last >= 0) {
-                lb = load_index(p.cu, p.cu64, last);
-                le = load_index(p.cu, p.cu64, last + 1);
+            const int64_t last = seqs.at(r1 - 1);
+            ok = last >= 0;
+            if (ok) {
+                lb = seqs.begin(last);
+                le = seqs.begin(last + 1);
                 ok = lb >= 0 && lb <= le && le <= p.rows;
-            } else {
-                ok = false;
             }
         }
         if (ok && r1 > lb && r1 < le && r1 < lb + W - 1) stop = lb + W - 1 < le ? lb + W - 1 : le;
     }
-    if (c0 >= p.dim || r >= stop) return;
-
-    float w[W][VEC], bias[VEC], u[W - 1][VEC];
-    load_taps<T, VEC, W>(p, c0, w, bias);
-    const T* x = static_cast<const T*>(p.x) + c0;
-    T* out = static_cast<T*>(p.out) + c0;
-    T* state = static_cast<T*>(p.state) + c0;
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k) {
-        // In the middle of a sequence the rows before r are all its own.
-        const int64_t q = r - (W - 1) + k;
-        if (b >= 0 && slot >= 0 && r < end && q >= begin) {
-            R::widen(R::load(x + q * p.x_stride), u[k]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) u[k][i] = 0.f;
-        }
+    if (r >= stop) return;
+    if (r != r0) {
+        request_before(r);
+        request(r, p.rows);
     }
 
-    for (; r < stop; r += kBatch) {
-        typename R::type raw[kBatch];
+    float w[W][VEC], bias[VEC], u[W - 1][VEC];
+    taps_in.widen(p, w, bias);
+    T* out = static_cast<T*>(p.out) + c;
+    T* state = static_cast<T*>(p.state) + c;
+    // In the middle of a sequence the rows before r are its own; else they are replaced.
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int64_t row = r + j < stop ? r + j : stop - 1;
-            raw[j] = R::load(x + row * p.x_stride);
-        }
+    for (int k = 0; k < W - 1; ++k) R::widen(before[k], u[k]);
+
+    const int64_t first = r;
+    for (; r < stop; r += kBatch) {
+        if (r != first) request(r, stop);
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             const int64_t row = r + j;
@@ -154,7 +219,7 @@ __global__ __launch_bounds__(kThreads) void conv_varlen_kernel(const ConvParams 
             if (row == begin) {
                 // The history, and the history that the sequence leaves behind.
                 T* h = state + slot * p.slot_stride;
-                const bool has = p.has && p.has[b];
+                const bool has = seqs.has_at(b);
                 typename R::type old[W - 1];
 #pragma unroll
                 for (int k = 0; k < W - 1; ++k) {
@@ -174,13 +239,13 @@ __global__ __launch_bounds__(kThreads) void conv_varlen_kernel(const ConvParams 
                         for (int i = 0; i < W - 1; ++i)
                             if (i == from + W - 1) v = old[i];
                     }
-                    R::store(h + k * p.dim, v);
+                    if (inside) R::store(h + k * p.dim, v);
                 }
             }
             float now[VEC], y[VEC];
             R::widen(raw[j], now);
             taps<VEC, W>(w, bias, u, now, p.silu, y);
-            R::store_through(out + row * p.out_stride, R::narrow(y));
+            if (inside) R::store_through(out + row * p.out_stride, R::narrow(y));
 #pragma unroll
             for (int k = 0; k + 1 < W - 1; ++k)
 #pragma unroll
@@ -192,7 +257,11 @@ __global__ __launch_bounds__(kThreads) void conv_varlen_kernel(const ConvParams 
 }
 
 // Single tokens. A wave takes one channel block of `tile` sequences, one after the
-// other, with the taps held over all of them.
+// other, with the taps held over all of them. Memory bounds it: 512 sequences of 10,240
+// channels in bf16 (84 MB) take 17 us on histories that no cache holds, 4.8 TB/s (20 us with
+// histories that the caches keep: the next step finds other layers' there), with two
+// sequences per wave (1 us less than one; four are no better). Small batches are
+// latency and take one.
 template <typename T, int VEC, int W>
 __global__ __launch_bounds__(kThreads) void conv_update_kernel(const ConvParams p) {
     typedef Raw<T, VEC> R;
@@ -203,8 +272,9 @@ __global__ __launch_bounds__(kThreads) void conv_update_kernel(const ConvParams 
     const int64_t c0 = (wave % p.channel_blocks) * (64 * VEC) + lane * VEC;
     const int64_t b0 = wave / p.channel_blocks * p.tile;
     if (c0 >= p.dim) return;
+    Taps<T, VEC, W> taps_in;
+    taps_in.request(p, c0);
     float w[W][VEC], bias[VEC];
-    load_taps<T, VEC, W>(p, c0, w, bias);
     const T* x = static_cast<const T*>(p.x) + c0;
     T* out = static_cast<T*>(p.out) + c0;
     T* state = static_cast<T*>(p.state) + c0;
@@ -214,16 +284,17 @@ __global__ __launch_bounds__(kThreads) void conv_update_kernel(const ConvParams 
         T* h = state + slot * p.slot_stride;
         typename R::type old[W - 1], fresh = R::load(x + b * p.x_stride);
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) old[k] = R::load(h + k * p.dim);
+        for (int k = 0; k < W - 1; ++k) old[k] = R::load_through(h + k * p.dim);
         float u[W - 1][VEC], now[VEC], y[VEC];
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) R::widen(old[k], u[k]);
         R::widen(fresh, now);
+        taps_in.widen(p, w, bias);
         taps<VEC, W>(w, bias, u, now, p.silu, y);
         R::store(out + b * p.out_stride, R::narrow(y));
 #pragma unroll
-        for (int k = 0; k + 1 < W - 1; ++k) R::store(h + k * p.dim, old[k + 1]);
-        R::store(h + (W - 2) * p.dim, fresh);
+        for (int k = 0; k + 1 < W - 1; ++k) R::store_through(h + k * p.dim, old[k + 1]);
+        R::store_through(h + (W - 2) * p.dim, fresh);
     }
 }
 
@@ -319,7 +390,7 @@ int launch(const ssu_conv_args* a, hipStream_t stream, const char* entry) {
     p.slot64 = a->slot_dtype == SSU_I64;
     p.silu = a->silu != 0;
     const int64_t blocks = (a->dim + 64 * VEC - 1) / (64 * VEC);
-    p.tile = VARLEN ? 16 : 1;
+    p.tile = VARLEN ? ((a->rows + 15) / 16 * blocks >= 2048 ? 16 : 4) : (a->rows * blocks >= 8192 ? 2 : 1);
     const int64_t tiles = (a->rows + p.tile - 1) / p.tile;
     if (blocks > INT32_MAX || tiles * blocks > static_cast<int64_t>(INT32_MAX) * kWaves)
         return ssu::report(SSU_ERR_UNSUPPORTED, "%s: too many rows for one launch", entry);
