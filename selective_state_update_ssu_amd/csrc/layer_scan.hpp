@@ -74,7 +74,8 @@ struct ScanParams {
 __device__ __forceinline__ float softplus_fast(float v) {
     const float e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(v));
     const float u = 1.f + e;
-    return fmaxf(v, 0.f) + fmaf(__builtin_amdgcn_logf(u), kLn2, e - (u - 1.f));
+    return __builtin_amdgcn_fmed3f(v, 0.f, __builtin_inff()) +
+           fmaf(__builtin_amdgcn_logf(u), kLn2, e - (u - 1.f));
 }
 
 // Element i of a state of storage type `dtype`, and its store (to nearest).
@@ -338,8 +339,11 @@ __global__ __launch_bounds__(64 * scan_waves(N)) void scan_kernel(const ScanPara
     if (kTile < rows) load(kTile, raw);
     lds_barrier();
 
-    for (int t0 = 0, buf = 0; t0 < rows; t0 += kTile, buf ^= 1) {
-        float next_dx[kOwn], next_gate[kOwn];
+    // One tile, with the next one prepared meanwhile; `which` is its half of the buffers. Two
+    // copies of the body take turns, so that nothing moves between registers.
+    const auto tile = [&](int t0, auto which, float (&dx)[kOwn], float (&gate)[kOwn],
+                          float (&next_dx)[kOwn], float (&next_gate)[kOwn]) {
+        constexpr int buf = which.value;
         if (t0 + kTile < rows) stage(t0 + kTile, raw, buf ^ 1, next_dx, next_gate);
         if (t0 + 2 * kTile < rows) load(t0 + 2 * kTile, raw);
 
@@ -373,10 +377,15 @@ __global__ __launch_bounds__(64 * scan_waves(N)) void scan_kernel(const ScanPara
                 if (t0 + t < rows && active)
                     (static_cast<IT*>(p.out) + (piece.row + t0 + t) * p.out_stride)[c] =
                         static_cast<IT>(y);
-                dx[j] = next_dx[j];
-                gate[j] = next_gate[j];
             }
         }
+    };
+    float other_dx[kOwn], other_gate[kOwn];
+    for (int t0 = 0; t0 < rows; t0 += kTile) {
+        tile(t0, std::integral_constant<int, 0>(), dx, gate, other_dx, other_gate);
+        t0 += kTile;
+        if (t0 >= rows) break;
+        tile(t0, std::integral_constant<int, 1>(), other_dx, other_gate, dx, gate);
     }
 
     if constexpr (OUT) {
