@@ -158,8 +158,8 @@ __device__ __forceinline__ Piece find_piece(const ScanParams& p, int64_t i) {
         int64_t before = 0;  // pieces of the sequences before
         for (int64_t b0 = 0; b0 < p.nseq; b0 += 64) {
             int64_t begin = 0, len = b0 + lane < p.nseq ? sequence(p, b0 + lane, &begin) : 0;
-            const int piece_rows = static_cast<int>(p.piece);
-            const int count = (static_cast<int>(len) + piece_rows - 1) / piece_rows;
+            const unsigned piece_rows = static_cast<unsigned>(p.piece);
+            const int count = static_cast<int>((static_cast<unsigned>(len) + piece_rows - 1) / piece_rows);
             int upto = count;  // of lanes 0 .. lane
 #pragma unroll
             for (int d = 1; d < 64; d *= 2) {

@@ -581,3 +581,19 @@ def test_binding_refusals():
             call()
     torch.cuda.synchronize()
     assert count.tolist() == [0] * 4
+
+
+def test_serving_example():
+    """The example's run: packed prompts, forks, decoding and compaction together give each
+    request the scores of a run alone. The library's calls are row by row the same but for the
+    join of pieces; the projections are torch's bf16 products, whose shapes differ
+    between the two runs: a few bf16 roundings (2^-8 each) of the largest score over the
+    layers, far from what a wrong slot would give."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "state_space_serving.py")
+    spec = importlib.util.spec_from_file_location("state_space_serving", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    assert module.main(layers=3, dim=256, tokens=10) < 10 * 2.0 ** -8
