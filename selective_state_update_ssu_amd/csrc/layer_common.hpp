@@ -108,6 +108,13 @@ __device__ __forceinline__ int64_t count_starts(const void* cu, int is64, int64_
     return lo;
 }
 
+// The 64-bit value of lane i, the same for the whole wave.
+__device__ __forceinline__ int64_t lane64(int64_t v, int i) {
+    const unsigned lo = __builtin_amdgcn_readlane(static_cast<unsigned>(v), i);
+    const unsigned hi = __builtin_amdgcn_readlane(static_cast<unsigned>(v >> 32), i);
+    return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
 // ------------------------------------------------------------------ host checks
 
 inline bool is_dtype(int32_t d) { return d == SSU_F32 || d == SSU_F16 || d == SSU_BF16; }

@@ -97,11 +97,6 @@ struct Sequences {
             }
         }
     }
-    static __device__ __forceinline__ int64_t lane64(int64_t v, int64_t i) {
-        const unsigned lo = __builtin_amdgcn_readlane(static_cast<unsigned>(v), static_cast<int>(i));
-        const unsigned hi = __builtin_amdgcn_readlane(static_cast<unsigned>(v >> 32), static_cast<int>(i));
-        return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
-    }
     // The last sequence that starts at or before `row`, or -1.
     __device__ __forceinline__ int64_t at(int64_t row) const {
         if (!few) return ssu::uniform64(count_starts(p.cu, p.cu64, p.nseq, row) - 1);
@@ -109,10 +104,10 @@ struct Sequences {
         return __builtin_popcountll(__ballot(in)) - 1;
     }
     __device__ __forceinline__ int64_t begin(int64_t i) const {
-        return few ? lane64(start, i) : ssu::uniform64(load_index(p.cu, p.cu64, i));
+        return few ? lane64(start, static_cast<int>(i)) : ssu::uniform64(load_index(p.cu, p.cu64, i));
     }
     __device__ __forceinline__ int64_t slot_at(int64_t i) const {
-        return few ? lane64(slot, i) : ssu::uniform64(slot_of(p, i));
+        return few ? lane64(slot, static_cast<int>(i)) : ssu::uniform64(slot_of(p, i));
     }
     __device__ __forceinline__ bool has_at(int64_t i) const {
         return few ? __builtin_amdgcn_readlane(has, static_cast<int>(i)) : p.has && p.has[i];

@@ -38,7 +38,9 @@ struct Piece {
     int64_t seq;
     int64_t index, count; // of this piece in its sequence, and its sequence's pieces
     int64_t row;          // first packed row
+    int64_t slot;
     int rows;
+    bool has;             // the sequence has an initial state
 };
 
 struct ScanParams {
@@ -110,12 +112,29 @@ __device__ __forceinline__ scan_args* fresh_args() {
     return a;
 }
 
-// The rows of sequence b; none if it is inert.
-__device__ __forceinline__ int64_t sequence(const ScanParams& p, int64_t b, int64_t* begin) {
-    *begin = load_index(p.cu, p.cu64, b);
-    const int64_t end = load_index(p.cu, p.cu64, b + 1);
-    return *begin >= 0 && *begin <= end && end <= p.rows && scan_slot(p, b) >= 0 ? end - *begin : 0;
-}
+// What a lane knows of sequence b; no rows if it is inert. The reads do not wait for each
+// other: a short call is little else than dependent reads.
+struct Sequence {
+    int64_t begin = 0, slot = -1;
+    int rows = 0, has = 0;
+    __device__ __forceinline__ Sequence() {}
+    __device__ __forceinline__ Sequence(const ScanParams& p, int64_t b) {
+        begin = load_index(p.cu, p.cu64, b);
+        const int64_t end = load_index(p.cu, p.cu64, b + 1);
+        slot = scan_slot(p, b);
+        has = p.has ? p.has[b] : 0;
+        rows = begin >= 0 && begin <= end && end <= p.rows && slot >= 0 ? static_cast<int>(end - begin) : 0;
+    }
+    // Lane l's, for the whole wave.
+    __device__ __forceinline__ Sequence of_lane(int l) const {
+        Sequence s;
+        s.begin = lane64(begin, l);
+        s.slot = lane64(slot, l);
+        s.rows = __builtin_amdgcn_readlane(rows, l);
+        s.has = __builtin_amdgcn_readlane(has, l);
+        return s;
+    }
+};
 
 // Place of workgroup `id` of `n` in a list that goes from long to short work, when all
 // are resident at once: workgroups reach the compute units in rounds of kUnits, and every
@@ -137,29 +156,32 @@ __device__ __forceinline__ Piece find_piece(const ScanParams& p, int64_t i) {
     q.seq = -1;
     q.index = 0;
     q.count = 1;
-    q.row = 0;
-    q.rows = 0;
+    Sequence s;
     if (p.piece == 0) {
         int64_t b = i;
         if (p.nseq <= 64) {
-            int64_t begin, len = lane < p.nseq ? sequence(p, lane, &begin) : -1;
-            const int mine = static_cast<int>(len);
+            Sequence mine;
+            if (lane < p.nseq) mine = Sequence(p, lane);
             int rank = 0;
             for (int j = 0; j < p.nseq; ++j) {
-                const int other = __builtin_amdgcn_readlane(mine, j);
-                rank += other > mine || (other == mine && j < lane);
+                const int other = __builtin_amdgcn_readlane(mine.rows, j);
+                rank += other > mine.rows || (other == mine.rows && j < lane);
             }
             b = __builtin_ctzll(__ballot(rank == i && lane < p.nseq) | 1ull << 63);
+            s = mine.of_lane(static_cast<int>(b));
+        } else {
+            s = Sequence(p, b).of_lane(0);
         }
-        const int64_t len = sequence(p, b, &q.row);
-        if (len > 0) q.seq = b;
-        q.rows = static_cast<int>(len);
+        if (s.rows > 0) q.seq = b;
+        q.row = s.begin;
+        q.rows = s.rows;
     } else {
+        const unsigned piece_rows = static_cast<unsigned>(p.piece);
         int64_t before = 0;  // pieces of the sequences before
         for (int64_t b0 = 0; b0 < p.nseq; b0 += 64) {
-            int64_t begin = 0, len = b0 + lane < p.nseq ? sequence(p, b0 + lane, &begin) : 0;
-            const unsigned piece_rows = static_cast<unsigned>(p.piece);
-            const int count = static_cast<int>((static_cast<unsigned>(len) + piece_rows - 1) / piece_rows);
+            Sequence mine;
+            if (b0 + lane < p.nseq) mine = Sequence(p, b0 + lane);
+            const int count = static_cast<int>((static_cast<unsigned>(mine.rows) + piece_rows - 1) / piece_rows);
             int upto = count;  // of lanes 0 .. lane
 #pragma unroll
             for (int d = 1; d < 64; d *= 2) {
@@ -169,25 +191,27 @@ __device__ __forceinline__ Piece find_piece(const ScanParams& p, int64_t i) {
             const unsigned long long past = __ballot(before + upto > i);
             if (past) {
                 const int l = __builtin_ctzll(past);
+                s = mine.of_lane(l);
                 q.seq = b0 + l;
                 q.count = __builtin_amdgcn_readlane(count, l);
                 q.index = i - before - __builtin_amdgcn_readlane(upto, l) + q.count;
-                len = sequence(p, q.seq, &begin);
-                q.row = begin + q.index * p.piece;
-                len -= q.index * p.piece;
-                q.rows = static_cast<int>(len < p.piece ? len : p.piece);
                 // Decreasing cu_seqlens may name more pieces than the scratch holds.
                 if (i - q.index + q.count > p.pieces) q.seq = -1;
                 break;
             }
             before += __builtin_amdgcn_readlane(upto, 63);
         }
+        q.row = s.begin + q.index * p.piece;
+        const int64_t left = s.rows - q.index * p.piece;
+        q.rows = static_cast<int>(left < p.piece ? left : p.piece);
     }
     q.seq = ssu::uniform64(q.seq);
     q.index = ssu::uniform64(q.index);
     q.count = ssu::uniform64(q.count);
     q.row = ssu::uniform64(q.row);
     q.rows = __builtin_amdgcn_readfirstlane(q.rows);
+    q.slot = ssu::uniform64(s.slot);
+    q.has = __builtin_amdgcn_readfirstlane(s.has) != 0;
     return q;
 }
 
@@ -235,17 +259,11 @@ __global__ __launch_bounds__(64 * scan_waves(N)) void scan_kernel(const ScanPara
     const int c = g * p.group_dim + (active ? in_group : p.group_dim - 1);
     const int n0 = wave * NW;
     const bool last = piece.index + 1 == piece.count;
-    const bool has = p.has && p.has[piece.seq];
+    const bool has = piece.has;
     const int64_t at_end = static_cast<int64_t>(c) * N + n0;
-    const int64_t at_state = scan_slot(p, piece.seq) * p.slot_stride + at_end;
+    const int64_t at_state = piece.slot * p.slot_stride + at_end;
     const int64_t ends_size = static_cast<int64_t>(p.dim) * N;
 
-    float A[NW], s[NW];
-#pragma unroll
-    for (int i = 0; i < NW; ++i) {
-        A[i] = p.A[at_end + i] * kLog2e;
-        s[i] = 0.f;
-    }
     if (!OUT && last) {
         // The second pass's last piece overwrites the slot that its first piece
         // starts from: keep the entering state beside the end states.
@@ -256,29 +274,6 @@ __global__ __launch_bounds__(64 * scan_waves(N)) void scan_kernel(const ScanPara
                     has ? state_load(p.state, p.state_dtype, at_state + i) : 0.f;
         return;
     }
-    if (piece.index == 0) {
-        if (has) {
-            if (OUT && piece.count > 1) {
-                const float* from = p.ends + (pi + piece.count - 1) * ends_size + at_end;
-#pragma unroll
-                for (int i = 0; i < NW; ++i) s[i] = from[i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < NW; ++i) s[i] = state_load(p.state, p.state_dtype, at_state + i);
-            }
-        }
-    } else if (OUT) {
-        // End state of piece 0 (which holds the entering state), then the others'.
-#pragma unroll NW <= 8 ? 4 : 1
-        for (int64_t k = pi - piece.index; k < pi; ++k) {
-            const float* from = p.ends + k * ends_size + at_end;
-            const float sum = p.sums[k * p.dim + c];
-#pragma unroll
-            for (int i = 0; i < NW; ++i)
-                s[i] = fmaf(__builtin_amdgcn_exp2f(A[i] * sum), s[i], from[i]);
-        }
-    }
-
     const float bias = p.dt_bias ? p.dt_bias[c] : 0.f;
     const float skip = OUT && p.D ? p.D[c] : 0.f;
     const bool softplus = p.softplus;
@@ -332,10 +327,43 @@ __global__ __launch_bounds__(64 * scan_waves(N)) void scan_kernel(const ScanPara
                 bs[buf][bc_row + j * kStep][bc_col] = widen_io<IT>(in.bc[j]);
     };
 
+    // The first tile is on its way while the state is made.
     In raw;
     float dx[kOwn], gate[kOwn];
     load(0, raw);
+    float A[NW], s[NW];
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+        A[i] = p.A[at_end + i] * kLog2e;
+        s[i] = 0.f;
+    }
+    if (piece.index == 0) {
+        if (has) {
+            if (OUT && piece.count > 1) {
+                const float* from = p.ends + (pi + piece.count - 1) * ends_size + at_end;
+#pragma unroll
+                for (int i = 0; i < NW; ++i) s[i] = from[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < NW; ++i) s[i] = state_load(p.state, p.state_dtype, at_state + i);
+            }
+        }
+    } else if (OUT) {
+        // End state of piece 0 (which holds the entering state), then the others'.
+#pragma unroll NW <= 8 ? 4 : 1
+        for (int64_t k = pi - piece.index; k < pi; ++k) {
+            const float* from = p.ends + k * ends_size + at_end;
+            const float sum = p.sums[k * p.dim + c];
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+                s[i] = fmaf(__builtin_amdgcn_exp2f(A[i] * sum), s[i], from[i]);
+        }
+    }
+
     stage(0, raw, 0, dx, gate);
+    // vmcnt(0): state and A have arrived. Left to their first use, inside the loop, the wait
+    // for them would wait for every tile's inputs just requested.
+    __builtin_amdgcn_s_waitcnt(0x0f70);
     if (kTile < rows) load(kTile, raw);
     lds_barrier();
 
