@@ -379,16 +379,18 @@ std::vector<ssu_cache_block> blocks(PyObject* caches, int64_t nslots, at::Device
         const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq);
         out.reserve(n);
         for (Py_ssize_t i = 0; i < n; ++i) {
-            const std::string name = "caches[" + std::to_string(i) + "]";
-            const Tensor& c = tensor(name.c_str(), PySequence_Fast_GET_ITEM(seq, i));
+            const auto name = [i] { return "caches[" + std::to_string(i) + "]"; };
+            PyObject* item = PySequence_Fast_GET_ITEM(seq, i);
+            if (!THPVariable_Check(item)) value_error(name() + " must be a tensor");
+            const Tensor& c = THPVariable_Unpack(item);
             if (c.dim() < 1 || c.size(0) != nslots)
-                value_error(name + " must be [" + std::to_string(nslots) + ", ...], got " +
+                value_error(name() + " must be [" + std::to_string(nslots) + ", ...], got " +
                             list(c.sizes()));
-            same_device(name.c_str(), c, device);
+            if (c.device() != device) same_device(name().c_str(), c, device);
             const int64_t numel = nslots ? c.numel() / nslots : 0, size = c.element_size();
-            const int64_t stride = c.is_contiguous() ? numel : slots_of(name.c_str(), c);
+            const int64_t stride = c.is_contiguous() ? numel : slots_of(name().c_str(), c);
             if (stride < numel)
-                value_error(name + "'s slots overlap, got strides " + list(c.strides()));
+                value_error(name() + "'s slots overlap, got strides " + list(c.strides()));
             out.push_back({c.data_ptr(), numel * size, stride * size});
         }
     } catch (...) {

@@ -114,9 +114,10 @@ __global__ __launch_bounds__(kScan) void plan_kernel(int32_t* refcount, int64_t 
 
 constexpr int kThreads = 256;
 constexpr int kDepth = 4;                              // loads in flight per lane and pair
-constexpr int kPairs = 4;                              // neighbouring pairs of a workgroup
+constexpr int kPairs = 4;                              // neighbouring pairs of a workgroup, where there are many
 constexpr int64_t kTile = kThreads * kDepth * 16;      // bytes of a slot per workgroup
 constexpr int64_t kMostItems = INT32_MAX / 2;          // (tile, group) pairs of one launch
+constexpr int64_t kFewItems = 1024;                    // (tile, pair) pairs
 constexpr int kMaxCaches = 32;                         // caches of one launch
 
 struct Block {
@@ -142,12 +143,13 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 // One tile of one slot (bytes [at, at + kTile) of it, cut at its end): the four
 // 16-byte pieces of a lane, or where a cache's slots are not 16-byte aligned its
 // bytes one by one.
-__device__ __forceinline__ void copy_tile(const Block& c, int64_t at, const int (&from)[kPairs],
-                                          const int (&to)[kPairs], bool wide) {
+template <int PAIRS>
+__device__ __forceinline__ void copy_tile(const Block& c, int64_t at, const int (&from)[PAIRS],
+                                          const int (&to)[PAIRS], bool wide) {
     if (wide) {
-        u32x4 v[kPairs][kDepth];
+        u32x4 v[PAIRS][kDepth];
 #pragma unroll
-        for (int k = 0; k < kPairs; ++k) {
+        for (int k = 0; k < PAIRS; ++k) {
             if (from[k] < 0) continue;
             if (k > 0 && from[k] == from[k - 1]) {
 #pragma unroll
@@ -163,7 +165,7 @@ __device__ __forceinline__ void copy_tile(const Block& c, int64_t at, const int 
             }
         }
 #pragma unroll
-        for (int k = 0; k < kPairs; ++k) {
+        for (int k = 0; k < PAIRS; ++k) {
             if (from[k] < 0) continue;
 #pragma unroll
             for (int j = 0; j < kDepth; ++j) {
@@ -175,7 +177,7 @@ __device__ __forceinline__ void copy_tile(const Block& c, int64_t at, const int 
         }
     } else {
         const int64_t end = at + kTile < c.slot_bytes ? at + kTile : c.slot_bytes;
-        for (int k = 0; k < kPairs; ++k) {
+        for (int k = 0; k < PAIRS; ++k) {
             if (from[k] < 0) continue;
             for (int64_t o = at + threadIdx.x; o < end; o += kThreads)
                 c.base[to[k] * c.stride + o] = c.base[from[k] * c.stride + o];
@@ -188,22 +190,23 @@ __device__ __forceinline__ void copy_tile(const Block& c, int64_t at, const int 
 // so, 545 us in the hardware's order, 811 us with one pair at a time. Plain loads and
 // stores take 510 us there and 145 instead of 136 us on 36 moves of 10.6 MB; kept are those
 // that leave the caches to others. (A copy streams at 5.4 TB/s, a fill at 5.6.)
+template <int PAIRS>
 __global__ __launch_bounds__(kThreads) void copy_kernel(const CopyParams p) {
     const int lane = threadIdx.x & 63;
     int64_t n = p.n;
     if (p.plan) n = p.plan[0] - p.first < n ? p.plan[0] - p.first : n;
     const int first_tile = lane < p.ncaches ? p.first_tile[lane] : 0x7fffffff;
-    const int items = static_cast<int>((n + kPairs - 1) / kPairs) * p.tiles;
+    const int items = static_cast<int>((n + PAIRS - 1) / PAIRS) * p.tiles;
     for (int k = blockIdx.x; k < items; k += gridDim.x) {
         const int item = static_cast<int>(ssu::xcd_tile(k, items));
         const int group = item / p.tiles, tile = item % p.tiles;
         const int ci = __builtin_popcountll(__ballot(first_tile <= tile)) - 1;
         const Block c = p.cache[ci];
         const int64_t in_slot = static_cast<int64_t>(tile - __builtin_amdgcn_readlane(first_tile, ci)) * kTile;
-        // Lane k < kPairs reads pair k's ids: one wait for all of them.
-        const int64_t mine = static_cast<int64_t>(group) * kPairs + lane, at = p.first + mine;
+        // Lane k < PAIRS reads pair k's ids: one wait for all of them.
+        const int64_t mine = static_cast<int64_t>(group) * PAIRS + lane, at = p.first + mine;
         int from_lane = -1, to_lane = -1;
-        if (lane < kPairs && mine < n) {
+        if (lane < PAIRS && mine < n) {
             const int64_t s = p.plan ? p.plan[1 + at] : load_index(p.src, p.src64, at);
             const int64_t d = p.plan ? p.plan[1 + p.half + at] : load_index(p.dst, p.dst64, at);
             if (s >= 0 && s < p.nslots && d >= 0 && d < p.nslots && s != d) {
@@ -211,9 +214,9 @@ __global__ __launch_bounds__(kThreads) void copy_kernel(const CopyParams p) {
                 to_lane = static_cast<int>(d);
             }
         }
-        int from[kPairs], to[kPairs];
+        int from[PAIRS], to[PAIRS];
 #pragma unroll
-        for (int k = 0; k < kPairs; ++k) {
+        for (int k = 0; k < PAIRS; ++k) {
             from[k] = __builtin_amdgcn_readlane(from_lane, k);
             to[k] = __builtin_amdgcn_readlane(to_lane, k);
         }
@@ -304,16 +307,22 @@ int copy(const ssu_cache_args* a, const int32_t* plan, const void* src, int src6
             ++p.ncaches;
         }
         if (p.ncaches == 0) continue;
+        // Few copies are latency: a pair per workgroup then (one request forked four ways over
+        // four small caches: 4.4 us against 5.9), else kPairs (527 us against 811).
+        const bool few = n * p.tiles <= kFewItems;
+        const int64_t pairs = few ? 1 : kPairs;
         // The kernel counts its items in 32 bits.
-        const int64_t most = kMostItems / p.tiles * kPairs;
+        const int64_t most = kMostItems / p.tiles * pairs;
         for (p.first = 0; p.first < n; p.first += most) {
             p.n = n - p.first < most ? n - p.first : most;
-            const int64_t items = (p.n + kPairs - 1) / kPairs * p.tiles;
+            const int64_t items = (p.n + pairs - 1) / pairs * p.tiles;
             // One item per workgroup, but for compactions, whose moves are known on the
             // device only and may be few: there the grid is bounded.
-            const int64_t grid = plan && items > 65536 ? 65536 : items;
-            hipLaunchKernelGGL(copy_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
-                               stream, p);
+            const dim3 grid(static_cast<unsigned>(plan && items > 65536 ? 65536 : items));
+            if (few)
+                hipLaunchKernelGGL(copy_kernel<1>, grid, dim3(kThreads), 0, stream, p);
+            else
+                hipLaunchKernelGGL(copy_kernel<kPairs>, grid, dim3(kThreads), 0, stream, p);
             if (int rc = launched(entry)) return rc;
         }
     }

@@ -350,6 +350,20 @@ def test_cache_copy(n, padded):
         assert same(a, b), i
 
 
+@pytest.mark.parametrize("ways", [1, 3, 4, 7])
+def test_cache_copy_many_pairs(ways):
+    """Enough copies that a workgroup takes four pairs, with sources named 1 to 7 times in a
+    row, pairs to skip among them and a last group that is not full."""
+    nslots, n = 700, 301
+    caches = cache_set(ways, nslots, [((3000,), F32), ((5,), torch.uint8), ((40, 100), BF16)])
+    gpu = on_gpu(caches)
+    src = [k // ways for k in range(n)]
+    dst = [399 + k if k % 11 else -1 for k in range(n)]
+    lh.copy(caches, src, dst)
+    ssu.cache_copy(gpu, torch.tensor(src, device=DEV), torch.tensor(dst, device=DEV))
+    assert all(same(a, b) for a, b in zip(gpu, caches))
+
+
 def test_cache_copy_many_caches():
     caches = cache_set(20, 6, [((k + 1, 16), F32) for k in range(70)] + [((0,), F32)])
     gpu = on_gpu(caches)
