@@ -10,7 +10,6 @@
 
 #include <ATen/ATen.h>
 #include <c10/hip/HIPStream.h>
-#include <torch/csrc/Device.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -252,7 +251,7 @@ PyObject* conv(PyObject* const* arg) {
 }
 
 // (state, x, dt, A, B, C, cu_seqlens, out, D, z, dt_bias, dt_softplus, has_initial_state,
-//  state_batch_indices, pad_slot_id, workspace, make_workspace) -> out
+//  state_batch_indices, pad_slot_id, workspace) -> out
 PyObject* scan(PyObject* const* arg) {
     const Tensor &state = tensor("state", arg[0]), &x = tensor("x", arg[1]),
                  &dt = tensor("dt", arg[2]), &A = tensor("A", arg[3]), &B = tensor("B", arg[4]),
@@ -318,14 +317,11 @@ PyObject* scan(PyObject* const* arg) {
                             " of at least scan_workspace_bytes(...) = " +
                             std::to_string(bytes + 255) + " bytes");
         } else if (bytes > 0) {
-            PyObject* where = THPDevice_New(device);
-            PyObject* made = where ? PyObject_CallFunction(arg[16], "On", where,
-                                                           static_cast<Py_ssize_t>(bytes))
-                                   : nullptr;
-            Py_XDECREF(where);
-            if (!made) throw Error{nullptr, ""};
-            workspace = THPVariable_Unpack(made);
-            Py_DECREF(made);
+            // The call's own, freed at its end in the stream's order: the passes hand each
+            // other states through it, so neither a call of another thread on this stream may
+            // write it between their launches, nor may a graph that recorded them lose it (its
+            // allocations come from the graph's memory).
+            workspace = at::empty({static_cast<int64_t>(bytes) + 255}, x.options().dtype(at::kByte));
         }
         if (workspace.defined()) {
             a.workspace = reinterpret_cast<void*>(
@@ -517,7 +513,7 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef methods[] = {method<conv, 10>("conv"),
-                         method<scan, 17>("scan"),
+                         method<scan, 16>("scan"),
                          method<cache_alloc, 2>("cache_alloc"),
                          method<cache_adjust, 3>("cache_adjust"),
                          method<cache_copy, 3>("cache_copy"),

@@ -29,7 +29,7 @@ import threading
 
 import torch
 
-from . import _cached_workspace, library, library_path
+from . import library, library_path
 
 __all__ = ["causal_conv1d_varlen", "causal_conv1d_update", "selective_scan_varlen",
            "selective_scan_update", "scan_workspace_bytes", "cache_alloc", "cache_free",
@@ -119,12 +119,13 @@ def selective_scan_varlen(state, x, dt, A, B, C, cu_seqlens, out=None, *, D=None
     range, are not written.
 
     Scratch: `scan_workspace_bytes(...)` bytes, taken from `workspace` (uint8) or, without
-    one, from the binding's buffer of this device and stream, which
-    `ssd_combined_fwd_varlen` uses too and `reset_ssd_workspaces()` frees."""
+    one, allocated for the call on its stream, so calls of several threads may share a
+    stream and a recorded call keeps its scratch with its graph. A caller's `workspace` serves
+    one call at a time and has to outlive the graphs that recorded it."""
     if cu_seqlens is None:
         raise ValueError("cu_seqlens must be a 1-D [sequences + 1] tensor")
     return _run("scan", stream, state, x, dt, A, B, C, cu_seqlens, out, D, z, dt_bias, dt_softplus,
-                has_initial_state, state_batch_indices, pad_slot_id, workspace, _cached_workspace)
+                has_initial_state, state_batch_indices, pad_slot_id, workspace)
 
 
 def selective_scan_update(state, x, dt, A, B, C, out=None, *, D=None, z=None, dt_bias=None,
@@ -133,7 +134,7 @@ def selective_scan_update(state, x, dt, A, B, C, out=None, *, D=None, z=None, dt
     """The scan's decode step: row b is one token of sequence b, whose state is slot
     state_batch_indices[b] (None: slot b), updated in place. Returns `out` [batch, dim]."""
     return _run("scan", stream, state, x, dt, A, B, C, None, out, D, z, dt_bias, dt_softplus, None,
-                state_batch_indices, pad_slot_id, None, None)
+                state_batch_indices, pad_slot_id, None)
 
 
 # -------------------------------------------------------------------- cache slots

@@ -611,3 +611,83 @@ def test_serving_example():
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     assert module.main(layers=3, dim=256, tokens=10) < 10 * 2.0 ** -8
+
+
+# ------------------------------------------------------------- scratch of the scan
+
+def cut_scan(seed, lengths=(90, 3, 140), dim=70):
+    """A scan in pieces: a call on its inputs, its starting state and the eager result."""
+    c = scan_inputs(seed, list(lengths), dim, 16, 1, BF16, F32, F32)
+    g = {k: v.to(DEV) if isinstance(v, torch.Tensor) else v for k, v in c.items()}
+    cu = torch.tensor(c["cu"], dtype=torch.int32, device=DEV)
+    assert ssu.scan_workspace_bytes(c["cu"][-1], len(lengths), dim, 16, 1) > 255
+
+    def call(state, out=None):
+        return ssu.selective_scan_varlen(state, g["x"], g["dt"], g["A"], g["B"], g["C"], cu, out,
+                                         D=g["D"], z=g["z"], dt_bias=g["dt_bias"], dt_softplus=True,
+                                         has_initial_state=g["has"], state_batch_indices=g["slots"])
+    state = g["state"].clone()
+    want = call(state)
+    torch.cuda.synchronize()
+    return call, g["state"], want, state
+
+
+def test_recorded_scratch_outlives_larger_calls():
+    """A graph of a scan in pieces, replayed after larger calls on its stream and a reset of
+    the prefill's buffers, with tensors made since then in whatever memory was free: the replays
+    give the eager result and leave those tensors alone."""
+    call, start, want, after = cut_scan(70)
+    larger = cut_scan(71, (300, 250), 200)
+    s = torch.cuda.Stream()
+    cached = dict(ssu._ssd_workspaces)
+    with torch.cuda.stream(s):
+        state = start.clone()
+        call(state)
+        torch.cuda.synchronize()
+        cg = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(cg, stream=s):
+            got = call(state)
+        larger[0](larger[1].clone())
+        assert ssu._ssd_workspaces == cached
+        ssu.reset_ssd_workspaces()
+        torch.cuda.synchronize()
+        size = ssu.scan_workspace_bytes(233, 3, 70, 16, 1)
+        others = [torch.full((n,), 77, dtype=torch.uint8, device=DEV)
+                  for n in (size, size, size - 255, size // 2, 4 * size) for _ in range(4)]
+        for i in range(4):
+            state.copy_(start)
+            cg.replay()
+            larger[0](larger[1].clone())
+            torch.cuda.synchronize()
+            assert same(got, want) and same(state, after), i
+            assert all(bool((t == 77).all()) for t in others), i
+
+
+def test_two_threads_on_one_stream():
+    """Two host threads repeat scans in pieces of different inputs on the same stream: every
+    result equals the single-threaded one bit for bit."""
+    import threading
+    runs = [cut_scan(72), cut_scan(73, (200, 20, 90), 70)]
+    side = torch.cuda.Stream()
+    results, errors = [[], []], []
+
+    def worker(i):
+        try:
+            call, start = runs[i][:2]
+            with torch.cuda.stream(side):
+                for _ in range(40):
+                    state = start.clone()
+                    results[i].append((call(state), state))
+        except Exception as e:  # reported below, on the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=worker, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for (_, _, want, after), got in zip(runs, results):
+        assert len(got) == 40
+        assert all(same(y, want) and same(s, after) for y, s in got)

@@ -295,3 +295,16 @@ def test_scan_keeps_its_exponentials_to_the_decays(asm):
             # One before the loop, one in each of its two copies of a tile's body, and one
             # for the sums of a first pass.
             assert len(re.findall(r"\ts_barrier", body)) <= 4, name
+
+
+def test_scan_scratch_is_the_calls_own():
+    """The scan's passes hand each other states through its scratch: it takes no part in the
+    prefill's buffers, which calls of a stream share and a larger call replaces."""
+    from selective_state_update_ssu_amd import layer
+    binding = layer._load()
+    assert not hasattr(layer, "_cached_workspace")
+    for n in (15, 17):
+        with pytest.raises(TypeError, match="number of arguments"):
+            binding.scan(*[None] * n)
+    with pytest.raises(ValueError, match="state must be a tensor"):
+        binding.scan(*[None] * 16)
