@@ -543,7 +543,9 @@ def commit_replayssm_ring_trackers(ring_start, prev_num_accepted, prev_query_len
 # Prefill scratch, one buffer per (device, stream): grown to the largest call
 # seen, reused by every later call on that stream (MATE page: the module keeps
 # its SSD workspaces across calls, because per-call scratch allocation is what
-# makes a wrapper expensive).
+# makes a wrapper expensive). A call recorded into a graph takes no part: its
+# replays use the recorded address for as long as the graph lives, so its
+# scratch is made for it alone, in the graph's own memory.
 _ssd_workspaces = {}
 
 
@@ -554,7 +556,14 @@ def ssd_workspace_bytes(nchunks, batch, nheads, headdim, dstate, ngroups, chunk_
                                                  ngroups, chunk_size)) + 255
 
 
+def _capturing(device):
+    with torch.cuda.device(device):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _cached_workspace(device, nbytes):
+    if _capturing(device):
+        return torch.empty(nbytes + 255, dtype=torch.uint8, device=device)
     key = (device.index if device.index is not None else torch.cuda.current_device(),
            torch.cuda.current_stream(device).cuda_stream)
     with _lock:
@@ -596,7 +605,8 @@ def ssd_combined_fwd_varlen(x, dt, A, B, C, chunk_size, cu_seqlens, cu_chunk_seq
     `workspace` the binding keeps one per (device, stream), grown to the largest
     call seen and reused, so repeated calls allocate only the returned states
     (and `out` when it is not given); calls on one stream are ordered, so they
-    can share it. `reset_ssd_workspaces()` frees them. A caller that runs
+    can share it. `reset_ssd_workspaces()` frees them. A call that is recorded into a
+    graph gets scratch of the graph's own instead. A caller that runs
     prefills concurrently on one stream's behalf, or wants the memory under its
     own control, passes a uint8 tensor of at least `ssd_workspace_bytes(...)`
     bytes as `workspace`. With static_scratch=True the call goes to

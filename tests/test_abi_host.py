@@ -414,3 +414,28 @@ def test_ssd_noalloc_host_checks(lib):
     msg = lib.ssu_last_error().decode()
     assert "static scratch holds" in msg and str(cap) in msg, msg
     assert n == 34, n
+
+
+def test_ssd_workspace_of_a_recorded_call_host(monkeypatch):
+    """A prefill recorded into a graph gets scratch of its own: later calls neither replace
+    nor share it, and it replaces no buffer of the calls outside."""
+    import types
+
+    import torch
+    capturing = [False]
+    empty = torch.empty
+    monkeypatch.setattr(ssu, "_ssd_workspaces", {})
+    monkeypatch.setattr(torch, "empty", lambda *s, dtype, device: empty(*s, dtype=dtype))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: types.SimpleNamespace(cuda_stream=5))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: __import__("contextlib").nullcontext())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    device = torch.device("cuda", 0)
+    outside = ssu._cached_workspace(device, 100)
+    capturing[0] = True
+    first, second = ssu._cached_workspace(device, 100), ssu._cached_workspace(device, 1000)
+    capturing[0] = False
+    assert first is not outside and first is not second and second.numel() == 1000 + 255
+    assert list(ssu._ssd_workspaces.values()) == [outside]
+    assert ssu._cached_workspace(device, 50) is outside
+    assert ssu._cached_workspace(device, 1000) is not second

@@ -90,3 +90,40 @@ def test_ssd_prefill_graph_replays_match_eager():
         torch.cuda.synchronize()
         assert _same_bits(o_graph, o_eager), f"replay {i}: out differs from the eager call"
         assert _same_bits(st_graph, st_eager), f"replay {i}: states differ from the eager call"
+
+
+def test_ssd_prefill_graph_outlives_larger_calls():
+    """A recorded prefill after larger calls on its stream and a reset of the cached buffers,
+    with tensors made since then in whatever memory was free: the replays give the eager result
+    and leave those tensors alone."""
+    w = wl.ssd("graph_ssd_kept", 24, lengths=[300, 5, 129], H=4, P=64, N=64, G=2, chunk=256,
+               device=DEV, with_init=True)
+    big = wl.ssd("graph_ssd_big", 25, lengths=[700, 600], H=8, P=64, N=64, G=2, chunk=256,
+                 device=DEV, with_init=True)
+    o_eager = torch.empty_like(w.x)
+    st_eager = ssu.ssd_combined_fwd_varlen(*w.args(), out=o_eager, **w.kwargs())
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        o_graph = torch.full_like(w.x, float("nan"))
+        ssu.ssd_combined_fwd_varlen(*w.args(), out=o_graph, **w.kwargs())
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            st_graph = ssu.ssd_combined_fwd_varlen(*w.args(), out=o_graph, **w.kwargs())
+        size = ssu.ssd_workspace_bytes(w.seq_idx.numel(), w.last_chunk_indices.numel(),
+                                       w.x.shape[1], w.x.shape[2], w.B.shape[2], w.B.shape[1],
+                                       w.chunk_size)
+        ssu.ssd_combined_fwd_varlen(*big.args(), **big.kwargs())
+        ssu.reset_ssd_workspaces()
+        torch.cuda.synchronize()
+        others = [torch.full((n,), 77, dtype=torch.uint8, device=DEV)
+                  for n in (size, size, size // 2, 4 * size) for _ in range(4)]
+        for i in range(REPLAYS):
+            o_graph.fill_(float("nan"))
+            g.replay()
+            ssu.ssd_combined_fwd_varlen(*big.args(), **big.kwargs())
+            torch.cuda.synchronize()
+            assert _same_bits(o_graph, o_eager), f"replay {i}: out differs from the eager call"
+            assert _same_bits(st_graph, st_eager), f"replay {i}: states differ"
+            assert all(bool((t == 77).all()) for t in others), f"replay {i}: memory of others"
