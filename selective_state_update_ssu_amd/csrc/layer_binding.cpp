@@ -9,6 +9,8 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/DeviceGuard.h>
+#include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -170,8 +172,12 @@ void sequences(Args& a, const Tensor& cu, const Tensor& has, const Tensor& slots
     }
 }
 
+// The tensors' GPU is made the current one for the call: a default stream's handle names the
+// default stream of whichever GPU is current.
 template <typename Args>
 void call(const char* entry, int (*f)(const Args*, void*), const Args& a, at::Device device) {
+    c10::OptionalDeviceGuard guard;
+    if (c10::hip::current_device() != device.index()) guard.reset_device(device);
     void* stream = c10::hip::getCurrentHIPStream(device.index()).stream();
     int rc;
     Py_BEGIN_ALLOW_THREADS

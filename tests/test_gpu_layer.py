@@ -691,3 +691,24 @@ def test_two_threads_on_one_stream():
     for (_, _, want, after), got in zip(runs, results):
         assert len(got) == 40
         assert all(same(y, want) and same(s, after) for y, s in got)
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two GPUs")
+def test_tensors_on_a_gpu_that_is_not_current():
+    """Calls on tensors of GPU 1 while GPU 0 is current run on GPU 1's stream and leave GPU 0
+    current."""
+    c = scan_inputs(80, [1] * 5, 64, 16, 1, BF16, F32, F32)
+    on = [{k: v.to(f"cuda:{d}") if isinstance(v, torch.Tensor) else v for k, v in c.items()}
+          for d in (0, 1)]
+    results = []
+    for g in on:
+        y = ssu.selective_scan_update(g["state"], g["x"], g["dt"], g["A"], g["B"], g["C"],
+                                      dt_bias=g["dt_bias"], dt_softplus=True,
+                                      state_batch_indices=g["slots"])
+        count = torch.zeros(4, dtype=torch.int32, device=y.device)
+        ids = ssu.cache_alloc(count, 2)
+        assert torch.cuda.current_device() == 0
+        assert y.device == ids.device == g["x"].device
+        torch.cuda.synchronize(y.device)
+        results.append([y.cpu(), g["state"].cpu(), ids.cpu(), count.cpu()])
+    assert all(same(a, b) for a, b in zip(*results))

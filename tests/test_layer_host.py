@@ -308,3 +308,13 @@ def test_scan_scratch_is_the_calls_own():
             binding.scan(*[None] * n)
     with pytest.raises(ValueError, match="state must be a tensor"):
         binding.scan(*[None] * 16)
+
+
+def test_binding_switches_to_the_tensors_gpu():
+    """The native binding holds a device guard over its launches (what it does with two GPUs is
+    a test of its own, which needs them)."""
+    from selective_state_update_ssu_amd import layer
+    layer._load()
+    names = subprocess.run(["nm", "-D", "--undefined-only", layer.binding_path()],
+                           capture_output=True, text=True, check=True).stdout
+    assert "device_guard_impl_registry" in names
