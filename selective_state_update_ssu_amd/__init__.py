@@ -49,6 +49,7 @@ __all__ = ["ssu_one_token", "ssu_packed_varlen", "prepare_one_token", "prepare_p
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIBRARY = os.path.join(_HERE, "_lib", "libssu_amd.so")
 _lib = None
+_several_gpus = False  # known once the library is loaded
 _lock = threading.Lock()
 
 _STATE_DTYPES = {torch.float32: _abi.SSU_F32, torch.float16: _abi.SSU_F16,
@@ -63,10 +64,11 @@ def library_path() -> str:
 
 def library() -> ctypes.CDLL:
     """The loaded HIP library (loaded on first use; raises if it is not built)."""
-    global _lib
+    global _lib, _several_gpus
     if _lib is None:
         with _lock:
             if _lib is None:
+                _several_gpus = torch.cuda.device_count() > 1
                 _lib = _abi.load(_LIBRARY)
     return _lib
 
@@ -198,9 +200,16 @@ def _index(name, t, device):
     return t, _INDEX_DTYPES[t.dtype]
 
 
-def _stream(device, stream):
+def _launch(fn, ref, device, stream):
+    """fn's status for the arguments at `ref` on `stream` (default: the current one of
+    `device`), with `device` current: a default stream's handle names the default
+    stream of whichever GPU is current, and the library's per-GPU data is the current
+    GPU's."""
+    if _several_gpus and torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _launch(fn, ref, device, stream)
     s = torch.cuda.current_stream(device) if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return fn(ref, ctypes.c_void_p(s.cuda_stream))
 
 
 def _on_stream(fn):
@@ -282,8 +291,7 @@ class PreparedCall:
 
     def __call__(self, stream=None):
         """Launch on `stream` (a torch.cuda.Stream; default: the current stream)."""
-        s = torch.cuda.current_stream(self._device) if stream is None else stream
-        rc = self._fn(self._ref, ctypes.c_void_p(s.cuda_stream))
+        rc = _launch(self._fn, self._ref, self._device, stream)
         if rc != _abi.SSU_OK:
             _raise(library(), rc, self._entry)
         return self.out
@@ -502,7 +510,7 @@ def update_replayssm_ring_trackers(ring_start, prev_num_accepted, prev_query_len
         if ring_buffer_len is None:
             raise ValueError("advancing needs ring_buffer_len")
         args.reset, args.logical_window, args.ring_buffer_len = 0, logical_window, ring_buffer_len
-    rc = lib.ssu_ring_update(ctypes.byref(args), _stream(ring_start.device, stream))
+    rc = _launch(lib.ssu_ring_update, ctypes.byref(args), ring_start.device, stream)
     if rc != _abi.SSU_OK:
         _raise(lib, rc, "ssu_ring_update")
 
@@ -533,7 +541,7 @@ def commit_replayssm_ring_trackers(ring_start, prev_num_accepted, prev_query_len
         raise ValueError("num_accepted_tokens and query_start_loc must share a dtype")
     args.num_accepted, args.query_start_loc, args.meta_dtype = _ptr(na), _ptr(qsl), na_dt
     args.logical_window, args.ring_buffer_len = logical_window, ring_buffer_len
-    rc = lib.ssu_ring_commit(ctypes.byref(args), _stream(ring_start.device, stream))
+    rc = _launch(lib.ssu_ring_commit, ctypes.byref(args), ring_start.device, stream)
     if rc != _abi.SSU_OK:
         _raise(lib, rc, "ssu_ring_commit")
 
@@ -729,7 +737,7 @@ def ssd_combined_fwd_varlen(x, dt, A, B, C, chunk_size, cu_seqlens, cu_chunk_seq
     args.return_intermediate_states = int(bool(return_intermediate_states))
     args.workspace, args.workspace_bytes = ws_ptr, ws_bytes
     entry = lib.ssu_ssd_prefill_noalloc if static_scratch else lib.ssu_ssd_prefill
-    rc = entry(ctypes.byref(args), _stream(device, stream))
+    rc = _launch(entry, ctypes.byref(args), device, stream)
     if rc != _abi.SSU_OK:
         _raise(lib, rc, entry.__name__)
     return states

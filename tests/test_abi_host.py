@@ -439,3 +439,36 @@ def test_ssd_workspace_of_a_recorded_call_host(monkeypatch):
     assert list(ssu._ssd_workspaces.values()) == [outside]
     assert ssu._cached_workspace(device, 50) is outside
     assert ssu._cached_workspace(device, 1000) is not second
+
+
+def test_calls_run_on_the_tensors_gpu_host(monkeypatch):
+    """A call on tensors of a GPU that is not current makes it current for the launch (a default
+    stream's handle does not name a GPU); on the current one it switches nothing."""
+    import contextlib
+    import types
+
+    import torch
+    current, seen = [0], []
+
+    @contextlib.contextmanager
+    def device(d):
+        before, current[0] = current[0], d.index
+        yield
+        current[0] = before
+
+    monkeypatch.setattr(ssu, "_several_gpus", True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda d: types.SimpleNamespace(cuda_stream=100 + d.index))
+
+    def entry(ref, stream):
+        seen.append((current[0], stream.value))
+        return _abi.SSU_OK
+
+    call = ssu.PreparedCall.__new__(ssu.PreparedCall)
+    call._entry, call._fn, call._ref, call.out = "ssu_one_token", entry, None, "out"
+    for index in (0, 1):
+        call._device = torch.device("cuda", index)
+        assert call() == "out" and call(types.SimpleNamespace(cuda_stream=7)) == "out"
+    assert seen == [(0, 100), (0, 7), (1, 101), (1, 7)] and current == [0]
