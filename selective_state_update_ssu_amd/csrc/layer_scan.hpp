@@ -80,6 +80,14 @@ __device__ __forceinline__ float softplus_fast(float v) {
            fmaf(__builtin_amdgcn_logf(u), kLn2, e - (u - 1.f));
 }
 
+// s 2^a, where 2^a may be out of range and the product is not: an infinite s stays infinite and
+// a zero one zero for every finite a.
+__device__ __forceinline__ float scale_exp2(float s, float a) {
+    if (!(fabsf(a) < __builtin_inff())) return __builtin_amdgcn_exp2f(a) * s;
+    const float b = __builtin_amdgcn_fmed3f(a, -4096.f, 4096.f), n = ceilf(b);
+    return ldexpf(__builtin_amdgcn_exp2f(b - n) * s, static_cast<int>(n));
+}
+
 // Element i of a state of storage type `dtype`, and its store (to nearest).
 __device__ __forceinline__ float state_load(const void* p, int dtype, int64_t i) {
     if (dtype == SSU_F32) return static_cast<const float*>(p)[i];
@@ -351,14 +359,28 @@ __global__ __launch_bounds__(64 * scan_waves(N)) void scan_kernel(const ScanPara
         }
     } else if (OUT) {
         // End state of piece 0 (which holds the entering state), then the others'.
-#pragma unroll NW <= 8 ? 4 : 1
-        for (int64_t k = pi - piece.index; k < pi; ++k) {
-            const float* from = p.ends + k * ends_size + at_end;
-            const float sum = p.sums[k * p.dim + c];
+        const auto join = [&](auto in_range) {
+            const int64_t first = pi - piece.index;
 #pragma unroll
-            for (int i = 0; i < NW; ++i)
-                s[i] = fmaf(__builtin_amdgcn_exp2f(A[i] * sum), s[i], from[i]);
-        }
+            for (int i = 0; i < NW; ++i) s[i] = p.ends[first * ends_size + at_end + i];
+#pragma unroll in_range.value && NW <= 8 ? 4 : 1
+            for (int64_t k = first + 1; k < pi; ++k) {
+                const float* from = p.ends + k * ends_size + at_end;
+                const float sum = p.sums[k * p.dim + c];
+#pragma unroll
+                for (int i = 0; i < NW; ++i)
+                    s[i] = in_range.value
+                               ? fmaf(__builtin_amdgcn_exp2f(A[i] * sum), s[i], from[i])
+                               : scale_exp2(s[i], A[i] * sum) + from[i];
+            }
+        };
+        join(std::true_type());
+        // A piece's factor may leave the range where the rows' did not: 0 times an infinite
+        // state, or infinity times a zero or small one. What came of it is not finite.
+        float check = 0.f;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) check = fmaf(s[i], 0.f, check);
+        if (__ballot(check != check)) join(std::false_type());
     }
 
     stage(0, raw, 0, dx, gate);

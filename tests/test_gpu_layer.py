@@ -712,3 +712,63 @@ def test_tensors_on_a_gpu_that_is_not_current():
         torch.cuda.synchronize(y.device)
         results.append([y.cpu(), g["state"].cpu(), ids.cpu(), count.cpu()])
     assert all(same(a, b) for a, b in zip(*results))
+
+
+# --------------------------------------------------- joins of pieces out of fp32's range
+
+def check_join(c, softplus=True):
+    """A scan in pieces against the definition: finite values within their bounds, and the
+    same infinities and NaNs in the states."""
+    state = c["state"].to(DEV)
+    out = gpu_scan(c, state, None, softplus=softplus).cpu()
+    ref, bound, written, after, s_bound, touched = lh.scan(
+        c["x"], c["dt"], c["A"], c["B"], c["C"], c["D"], c["z"], c["dt_bias"], softplus, c["cu"],
+        c["state"], c["slots"].tolist(), c["has"].tolist())
+    out, ref, bound = out[written], ref[written], bound[written]
+    fine = torch.isfinite(ref)
+    assert torch.equal(torch.isfinite(out), fine)
+    lh.check("out", out[fine], ref[fine], bound[fine])
+    got, after, s_bound = state.cpu()[touched], after[touched], s_bound[touched]
+    fine = torch.isfinite(after)
+    assert torch.equal(torch.isnan(got), torch.isnan(after))
+    assert torch.equal(got[~fine & ~torch.isnan(after)].double(), after[~fine & ~torch.isnan(after)])
+    lh.check("state", got[fine], after[fine], s_bound[fine])
+
+
+@pytest.mark.parametrize("dim,N", [(40, 16), (70, 64), (20, 256)])
+def test_join_keeps_infinite_states(dim, N):
+    """Infinite entering states over pieces whose decay underflows, though no row's does."""
+    c = scan_inputs(90, [300, 5, 200], dim, N, 1, F32, F32, F32, bias=False)
+    c["dt"] = c["dt"].abs() * 0.2 + 0.1
+    c["A"] = -Draw(91).uniform(0.5, 16.0, dim, N)
+    c["has"][:] = True
+    for b, slot in enumerate(c["slots"].tolist()):
+        c["state"][slot, b::3] = float("inf")
+        c["state"][slot, b + 4::5] = float("-inf")
+    check_join(c, softplus=False)
+
+
+def test_join_of_growing_states():
+    """Growth by up to e^144 a piece: states that are zero until late rows, and tiny ones that
+    grow into range."""
+    dim, N = 40, 16
+    c = scan_inputs(92, [300, 200], dim, N, 1, F32, F32, F32, bias=False)
+    c["dt"] = torch.full_like(c["dt"], 0.5)
+    c["A"] = Draw(93).uniform(2.0, 4.5, dim, N)
+    for b in range(2):
+        end = c["cu"][b + 1]
+        c["x"][c["cu"][b]:end - 3] = 0
+    c["has"][:] = False
+    check_join(c, softplus=False)
+    c["has"][:] = True
+    c["state"][:] = 0
+    check_join(c, softplus=False)
+    # Still, then e^91.2 in the second piece, then still: 2^-120 becomes 2^11.6.
+    c["A"].fill_(2.85)
+    c["dt"].zero_()
+    c["dt"][64:128] = 0.5
+    c["cu"] = [0, 200]
+    c["slots"], c["has"] = c["slots"][:1], c["has"][:1]
+    c["x"].zero_()
+    c["state"].fill_(2.0 ** -120)
+    check_join(c, softplus=False)
