@@ -81,11 +81,13 @@ __device__ __forceinline__ float softplus_fast(float v) {
 }
 
 // s 2^a, where 2^a may be out of range and the product is not: an infinite s stays infinite and
-// a zero one zero for every finite a.
+// a zero one zero for every finite a. Without a branch: one takes four registers more, which are
+// a quarter of the waves where a lane has 16 elements.
 __device__ __forceinline__ float scale_exp2(float s, float a) {
-    if (!(fabsf(a) < __builtin_inff())) return __builtin_amdgcn_exp2f(a) * s;
     const float b = __builtin_amdgcn_fmed3f(a, -4096.f, 4096.f), n = ceilf(b);
-    return ldexpf(__builtin_amdgcn_exp2f(b - n) * s, static_cast<int>(n));
+    const bool finite = fabsf(a) < __builtin_inff();
+    return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(finite ? b - n : a) * s,
+                                   finite ? static_cast<int>(n) : 0);
 }
 
 // Element i of a state of storage type `dtype`, and its store (to nearest).

@@ -318,3 +318,13 @@ def test_binding_switches_to_the_tensors_gpu():
     names = subprocess.run(["nm", "-D", "--undefined-only", layer.binding_path()],
                            capture_output=True, text=True, check=True).stdout
     assert "device_guard_impl_registry" in names
+
+
+def test_scan_of_16_elements_per_lane_keeps_its_waves(asm):
+    """States of 64 and 128 (16 elements per lane) with 16-bit io: four waves per SIMD take 128
+    registers each."""
+    for unit in ("layer_scan_f16.hip", "layer_scan_bf16.hip"):
+        found = re.findall(r"\.name:\s+_ZN5layer11scan_kernelI\S*?Li(64|128)ELi\d\S*"
+                           r".*?\.vgpr_count:\s+(\d+)", asm[unit], re.S)
+        assert len(found) == 12, unit
+        assert all(int(n) <= 128 for _, n in found), (unit, found)
