@@ -17,7 +17,8 @@
  * cu_seqlens[b + 1]); an empty range does nothing (its slot stays as it is), a
  * range outside [0, rows] or running backwards is inert. Device data is never
  * checked on the host. Preconditions, as in ssu.h: no two sequences share a slot,
- * cu_seqlens is non-decreasing, out overlaps no input.
+ * cu_seqlens is non-decreasing, out and the states overlap no other operand (checked
+ * on addresses; operands of one row stride may lie in disjoint columns of one buffer).
  */
 #ifndef SSU_LAYER_H
 #define SSU_LAYER_H

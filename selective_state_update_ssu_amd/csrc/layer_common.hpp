@@ -124,16 +124,28 @@ inline bool aligned(const void* p, int64_t a) {
     return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(a) == 0;
 }
 
-// Whether [a, a + abytes) and [b, b + bbytes) share a byte.
-inline bool overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
-    if (!a || !b || abytes <= 0 || bbytes <= 0) return false;
-    const auto a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + static_cast<uintptr_t>(bbytes) && b0 < a0 + static_cast<uintptr_t>(abytes);
-}
+// An operand's bytes: `n` rows of `width` bytes, `stride` bytes apart.
+struct Rows {
+    const void* p;
+    int64_t n, stride, width;
+    Rows(const void* base, int64_t rows, int64_t stride_elements, int64_t elements, int64_t esz)
+        : p(base), n(rows), stride(stride_elements * esz), width(elements * esz) {}
+    Rows(const void* base, int64_t bytes) : p(base), n(1), stride(0), width(bytes) {}
+    int64_t span() const { return n > 0 ? (n - 1) * stride + width : 0; }
+};
 
-// Bytes that `rows` rows of `width` elements, `stride` elements apart, span.
-inline int64_t span(int64_t rows, int64_t stride, int64_t width, int64_t esz) {
-    return rows > 0 ? ((rows - 1) * stride + width) * esz : 0;
+// Whether two operands share a byte; for those of unequal strides whether their spans do.
+inline bool overlap(const Rows& a, const Rows& b) {
+    if (!a.p || !b.p || a.span() <= 0 || b.span() <= 0) return false;
+    const auto a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+    if (a0 >= b0 + static_cast<uintptr_t>(b.span()) || b0 >= a0 + static_cast<uintptr_t>(a.span()))
+        return false;
+    // Rows of one stride (a single row has any): b's columns may lie beside a's.
+    const int64_t stride = a.n > 1 ? a.stride : b.stride;
+    if (stride <= 0 || (b.n > 1 && b.stride != stride)) return true;
+    const auto s = static_cast<uintptr_t>(stride);
+    const int64_t at = static_cast<int64_t>(b0 >= a0 ? (b0 - a0) % s : (s - (a0 - b0) % s) % s);
+    return at < a.width || at + b.width > stride;
 }
 
 inline int launched(const char* entry) {

@@ -337,19 +337,19 @@ int check(const ssu_conv_args* a, bool varlen) {
                           static_cast<const void*>(a->out), a->weight, a->bias})
         if (!aligned(q, esz))
             return report(SSU_ERR_INVALID_ARGUMENT, "operands must be aligned to their dtype");
-    const int64_t xb = span(a->rows, a->x_stride, a->dim, esz);
-    const int64_t ob = span(a->rows, a->out_stride, a->dim, esz);
-    const int64_t sb = span(a->nslots, a->slot_stride, (a->width - 1) * a->dim, esz);
-    const struct { const char* name; const void* p; int64_t bytes; } inputs[] = {
-        {"x", a->x, xb}, {"weight", a->weight, a->dim * a->width * esz},
-        {"bias", a->bias, a->dim * esz}};
+    const Rows out(a->out, a->rows, a->out_stride, a->dim, esz);
+    const Rows state(a->conv_state, a->nslots, a->slot_stride, (a->width - 1) * a->dim, esz);
+    const struct { const char* name; Rows rows; } inputs[] = {
+        {"x", Rows(a->x, a->rows, a->x_stride, a->dim, esz)},
+        {"weight", Rows(a->weight, a->dim * a->width * esz)},
+        {"bias", Rows(a->bias, a->dim * esz)}};
     for (const auto& in : inputs) {
-        if (overlap(a->out, ob, in.p, in.bytes))
+        if (overlap(out, in.rows))
             return report(SSU_ERR_INVALID_ARGUMENT, "out overlaps %s", in.name);
-        if (overlap(a->conv_state, sb, in.p, in.bytes))
+        if (overlap(state, in.rows))
             return report(SSU_ERR_INVALID_ARGUMENT, "conv_state overlaps %s", in.name);
     }
-    if (overlap(a->out, ob, a->conv_state, sb))
+    if (overlap(out, state))
         return report(SSU_ERR_INVALID_ARGUMENT, "out overlaps conv_state");
     return SSU_OK;
 }

@@ -100,26 +100,24 @@ int check(const ssu_scan_args* a, bool varlen) {
     if (a->rows == 0 || a->nseq == 0) return SSU_OK;
     const int64_t io = size_of(a->io_dtype), st = size_of(a->state_dtype),
                   dt = size_of(a->dt_dtype);
-    const int64_t state_bytes = span(a->nslots, a->slot_stride, a->dim * a->dstate, st);
-    const int64_t out_bytes = span(a->rows, a->out_stride, a->dim, io);
-    const struct { const char* name; const void* p; int64_t align, bytes; bool optional; } in[] = {
-        {"x", a->x, io, span(a->rows, a->x_stride, a->dim, io), false},
-        {"dt", a->dt, dt, span(a->rows, a->dt_stride, a->dim, dt), false},
-        {"B", a->B, io, span(a->rows, a->B_stride, gn, io), false},
-        {"C", a->C, io, span(a->rows, a->C_stride, gn, io), false},
-        {"A", a->A, 4, a->dim * a->dstate * 4, false},
-        {"z", a->z, io, span(a->rows, a->z_stride, a->dim, io), true},
-        {"D", a->D, 4, a->dim * 4, true},
-        {"dt_bias", a->dt_bias, 4, a->dim * 4, true},
-        {"cu_seqlens", a->cu_seqlens, a->cu_dtype == SSU_I64 ? 8 : 4,
-         (a->nseq + 1) * (a->cu_dtype == SSU_I64 ? 8 : 4), !varlen},
+    const struct { const char* name; int64_t align; Rows rows; bool optional; } in[] = {
+        {"x", io, Rows(a->x, a->rows, a->x_stride, a->dim, io), false},
+        {"dt", dt, Rows(a->dt, a->rows, a->dt_stride, a->dim, dt), false},
+        {"B", io, Rows(a->B, a->rows, a->B_stride, gn, io), false},
+        {"C", io, Rows(a->C, a->rows, a->C_stride, gn, io), false},
+        {"A", 4, Rows(a->A, a->dim * a->dstate * 4), false},
+        {"z", io, Rows(a->z, a->rows, a->z_stride, a->dim, io), true},
+        {"D", 4, Rows(a->D, a->dim * 4), true},
+        {"dt_bias", 4, Rows(a->dt_bias, a->dim * 4), true},
+        {"cu_seqlens", a->cu_dtype == SSU_I64 ? 8 : 4,
+         Rows(a->cu_seqlens, (a->nseq + 1) * (a->cu_dtype == SSU_I64 ? 8 : 4)), !varlen},
     };
     if (!a->state) return report(SSU_ERR_INVALID_ARGUMENT, "state must not be NULL");
     if (!a->out) return report(SSU_ERR_INVALID_ARGUMENT, "out must not be NULL");
     for (const auto& q : in) {
-        if (!q.p && !q.optional)
+        if (!q.rows.p && !q.optional)
             return report(SSU_ERR_INVALID_ARGUMENT, "%s must not be NULL", q.name);
-        if (!aligned(q.p, q.align))
+        if (!aligned(q.rows.p, q.align))
             return report(SSU_ERR_INVALID_ARGUMENT, "%s must be aligned to its dtype", q.name);
     }
     if (!aligned(a->out, io))
@@ -135,15 +133,16 @@ int check(const ssu_scan_args* a, bool varlen) {
                           "workspace must be 256-byte aligned and hold %lld bytes (got %zu)",
                           (long long)ws_bytes, a->workspace_bytes);
     }
-    const struct { const char* name; const void* p; int64_t bytes; } written[] = {
-        {"out", a->out, out_bytes}, {"state", a->state, state_bytes},
-        {"workspace", a->workspace, ws_bytes}};
+    const struct { const char* name; Rows rows; } written[] = {
+        {"out", Rows(a->out, a->rows, a->out_stride, a->dim, io)},
+        {"state", Rows(a->state, a->nslots, a->slot_stride, a->dim * a->dstate, st)},
+        {"workspace", Rows(a->workspace, ws_bytes)}};
     for (int i = 0; i < 3; ++i) {
         for (const auto& q : in)
-            if (overlap(written[i].p, written[i].bytes, q.p, q.bytes))
+            if (overlap(written[i].rows, q.rows))
                 return report(SSU_ERR_INVALID_ARGUMENT, "%s overlaps %s", written[i].name, q.name);
         for (int j = 0; j < i; ++j)
-            if (overlap(written[i].p, written[i].bytes, written[j].p, written[j].bytes))
+            if (overlap(written[i].rows, written[j].rows))
                 return report(SSU_ERR_INVALID_ARGUMENT, "%s overlaps %s", written[i].name,
                               written[j].name);
     }

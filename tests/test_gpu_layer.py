@@ -772,3 +772,33 @@ def test_join_of_growing_states():
     c["x"].zero_()
     c["state"].fill_(2.0 ** -120)
     check_join(c, softplus=False)
+
+
+def test_out_beside_inputs():
+    """out in columns of the buffer that holds x, for prompts and tokens: the results of a
+    buffer of its own."""
+    d = Draw(95)
+    rows, dim = 37, 64
+    cu = torch.tensor([0, 20, 37], dtype=torch.int32, device=DEV)
+    w = d.uniform(-0.5, 0.5, dim, 4).to(BF16).to(DEV)
+    wide = d.normal(rows, 3 * dim, io=BF16).to(DEV)
+    x, out, z = wide[:, :dim], wide[:, dim:2 * dim], wide[:, 2 * dim:]
+    c = scan_inputs(96, [20, 17], dim, 16, 1, BF16, F32, F32, nslots=2)
+    g = {k: v.to(DEV) if isinstance(v, torch.Tensor) else v for k, v in c.items()}
+    history, state = d.normal(2, 3, dim, io=BF16).to(DEV), g["state"]
+
+    def both(conv_out, scan_out, h, s):
+        u = ssu.causal_conv1d_varlen(h, x, w, cu, conv_out).clone()
+        y = ssu.selective_scan_varlen(s, x, g["dt"], g["A"], g["B"], g["C"], cu, scan_out, z=z).clone()
+        u1 = ssu.causal_conv1d_update(h, x[:2], w, None if conv_out is None else conv_out[:2]).clone()
+        y1 = ssu.selective_scan_update(s, x[:2], g["dt"][:2], g["A"], g["B"][:2], g["C"][:2],
+                                       None if scan_out is None else scan_out[:2], z=z[:2])
+        return [u, y, u1, y1.clone(), h, s]
+
+    before = wide.clone()
+    want = both(None, None, history.clone(), state.clone())
+    got = both(out, out, history.clone(), state.clone())
+    assert all(same(a, b) for a, b in zip(got, want))
+    assert same(x, before[:, :dim]) and same(z, before[:, 2 * dim:])
+    with pytest.raises(ValueError, match="out overlaps x"):
+        ssu.causal_conv1d_varlen(history, x, w, cu, wide[:, 1:dim + 1])

@@ -328,3 +328,29 @@ def test_scan_of_16_elements_per_lane_keeps_its_waves(asm):
                            r".*?\.vgpr_count:\s+(\d+)", asm[unit], re.S)
         assert len(found) == 12, unit
         assert all(int(n) <= 128 for _, n in found), (unit, found)
+
+
+def test_columns_of_one_buffer_do_not_overlap(lib):
+    """Operands in disjoint columns of rows of one buffer pass the overlap checks (the calls end at
+    a later refusal: too many rows or workgroups for one launch), touching ones do not."""
+    far = 1 << 56
+    many = dict(rows=1 << 40, x=far, x_stride=128, out_stride=128)
+    for out in (far + 128, far - 128, far + 256 * 7 + 128):
+        rc, msg = conv(lib, out=out, **many)
+        assert rc == UNS and "too many rows" in msg, (out - far, msg)
+    for out in (far + 126, far + 130, far, far - 126, far + 256 * 7):
+        rc, msg = conv(lib, out=out, **many)
+        assert rc == INV and "out overlaps x" in msg, (out - far, msg)
+    rc, msg = conv(lib, out=far + 128, **dict(many, x_stride=64))
+    assert rc == INV and "out overlaps x" in msg, msg
+
+    wide = dict(nseq=1 << 30, x_stride=256, out_stride=256, B_stride=256)
+    for kw in (dict(out=addr(2) + 128), dict(out=addr(2) + 192, B=addr(2) + 128),
+               dict(out=addr(2) - 192)):
+        rc, msg = scan(lib, **wide, **kw)
+        assert rc == _abi.SSU_ERR_LAUNCH and "launch failed" in msg, (kw, msg)
+    for kw, needle in ((dict(out=addr(2) + 126), "out overlaps x"),
+                       (dict(out=addr(2) + 192, B=addr(2) + 130), "out overlaps B"),
+                       (dict(out=addr(2) + 386), "out overlaps x")):
+        rc, msg = scan(lib, **wide, **kw)
+        assert rc == INV and needle in msg, (kw, msg)
