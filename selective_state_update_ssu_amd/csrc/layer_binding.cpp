@@ -12,6 +12,7 @@
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -412,7 +413,8 @@ PyObject* cache_alloc(PyObject* const* arg) {
     const Tensor& refcount = tensor("refcount", arg[0]);
     ssu_cache_args a = counts(refcount);
     a.n = integer(arg[1]);
-    if (a.n < 0) value_error("n must be >= 0, got " + std::to_string(a.n));
+    if (a.n < 0 || a.n > INT32_MAX)
+        value_error("n must be in [0, 2^31), got " + std::to_string(a.n));
     const Tensor out = ids(a.n, refcount.device());
     a.ids = static_cast<int32_t*>(out.data_ptr());
     call("ssu_cache_alloc", ssu_cache_alloc, a, refcount.device());
@@ -496,20 +498,19 @@ PyObject* cache_compact(PyObject* const* arg) {
     return THPVariable_Wrap(remap);
 }
 
-// Python entry of `f` with `count` positional arguments: no C++ exception leaves it.
+// Python entry of `f` with `count` positional arguments: no C++ exception leaves it. torch's
+// become what they are from any of its functions (torch.OutOfMemoryError among them).
 template <PyObject* (*f)(PyObject* const*), Py_ssize_t count>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
     try {
         if (n != count) throw Error{PyExc_TypeError, "wrong number of arguments"};
         return f(args);
     } catch (const Error& e) {
         if (e.kind) PyErr_SetString(e.kind, e.text.c_str());
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-    } catch (...) {
-        PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
+        return nullptr;
     }
-    return nullptr;
+    END_HANDLE_TH_ERRORS
 }
 
 template <PyObject* (*f)(PyObject* const*), Py_ssize_t count>

@@ -802,3 +802,19 @@ def test_out_beside_inputs():
     assert same(x, before[:, :dim]) and same(z, before[:, 2 * dim:])
     with pytest.raises(ValueError, match="out overlaps x"):
         ssu.causal_conv1d_varlen(history, x, w, cu, wide[:, 1:dim + 1])
+
+
+def test_allocation_errors_are_torchs():
+    """What does not fit raises torch.OutOfMemoryError, as torch's own calls do; more ids than any
+    cache has are refused before anything is allocated."""
+    x = torch.zeros(1, 512, dtype=BF16, device=DEV).expand(1 << 30, 512)
+    w = torch.zeros(512, 4, dtype=BF16, device=DEV)
+    state = torch.zeros(1, 3, 512, dtype=BF16, device=DEV)
+    cu = torch.tensor([0, 1 << 30], device=DEV)
+    with pytest.raises(torch.OutOfMemoryError):
+        ssu.causal_conv1d_varlen(state, x, w, cu)
+    count = torch.zeros(4, dtype=torch.int32, device=DEV)
+    for n in (1 << 31, 1 << 50):
+        with pytest.raises(ValueError, match="n must be"):
+            ssu.cache_alloc(count, n)
+    assert count.tolist() == [0] * 4
