@@ -70,37 +70,49 @@ def _binding_flags():
             f"-I{INCLUDE}", *[f"-isystem{p}" for p in include]]
 
 
+def _compile(cmd, src):
+    obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
+    return obj, _run([*cmd, "-c", os.path.join(CSRC, src), "-o", obj])
+
+
+def _link_binding(obj):
+    import torch
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    _run([CXX, "-shared", "-fPIC", "-o", BINDING + ".tmp", obj,
+          f"-L{LIB_DIR}", "-l:" + os.path.basename(LIBRARY), "-Wl,-rpath,$ORIGIN",
+          f"-L{torch_lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"])
+    os.replace(BINDING + ".tmp", BINDING)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source and link the library; returns its path."""
+    """Compile every source and link the library; returns its path. The Python binding comes
+    after it and needs torch and its headers: without torch the library is built alone."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
-
-    def compile_one(src):
-        obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-        if src == BINDING_SOURCE:
-            cmd = [CXX, *_binding_flags()]
-        else:
-            cmd = [HIPCC, *CXXFLAGS]
-        return obj, _run([*cmd, "-c", os.path.join(CSRC, src), "-o", obj])
-
-    sources = SOURCES + STREAM_SOURCES + [BINDING_SOURCE]
-    with ThreadPoolExecutor(max_workers=min(len(sources), os.cpu_count() or 1)) as ex:
-        results = list(ex.map(compile_one, sources))
-    for obj, msg in results:
-        if msg and verbose:
-            print(msg, file=sys.stderr)
-    objs = dict(zip(sources, (o for o, _ in results)))
+    sources = SOURCES + STREAM_SOURCES
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        torch = None
+    with ThreadPoolExecutor(max_workers=min(len(sources) + 1, os.cpu_count() or 1)) as ex:
+        jobs = {s: ex.submit(_compile, [HIPCC, *CXXFLAGS], s) for s in sources}
+        if torch is not None:
+            jobs[BINDING_SOURCE] = ex.submit(lambda: _compile([CXX, *_binding_flags()],
+                                                              BINDING_SOURCE))
+    objs = {s: jobs[s].result() for s in sources}
     for lib, srcs in ((LIBRARY, SOURCES), (STREAM_LIBRARY, STREAM_SOURCES)):
         tmp = lib + ".tmp"
         _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp,
-              *[objs[s] for s in srcs]])
+              *[objs[s][0] for s in srcs]])
         os.replace(tmp, lib)
-    import torch
-    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    _run([CXX, "-shared", "-fPIC", "-o", BINDING + ".tmp", objs[BINDING_SOURCE],
-          f"-L{LIB_DIR}", "-l:" + os.path.basename(LIBRARY), "-Wl,-rpath,$ORIGIN", f"-L{torch_lib}", "-ltorch_python", "-ltorch_cpu", "-lc10",
-          "-lc10_hip"])
-    os.replace(BINDING + ".tmp", BINDING)
+    if torch is not None:
+        objs[BINDING_SOURCE] = jobs[BINDING_SOURCE].result()
+        _link_binding(objs[BINDING_SOURCE][0])
+    else:
+        print(f"torch is not importable: {BINDING} is not built", file=sys.stderr)
+    for _, msg in objs.values():
+        if msg and verbose:
+            print(msg, file=sys.stderr)
     return LIBRARY
 
 

@@ -354,3 +354,29 @@ def test_columns_of_one_buffer_do_not_overlap(lib):
                        (dict(out=addr(2) + 386), "out overlaps x")):
         rc, msg = scan(lib, **wide, **kw)
         assert rc == INV and needle in msg, (kw, msg)
+
+
+@pytest.mark.parametrize("torch_there", [False, True])
+def test_build_of_the_library_does_not_need_the_binding(torch_there, monkeypatch, tmp_path):
+    """Without torch, or where the binding does not compile, the C library is still built."""
+    import sys
+    ran, moved = [], []
+
+    def run(cmd):
+        ran.append(cmd)
+        if any(c.endswith(build.BINDING_SOURCE) for c in cmd):
+            raise RuntimeError("the binding does not compile")
+        return ""
+
+    monkeypatch.setattr(build, "_run", run)
+    monkeypatch.setattr(build, "BUILD_DIR", str(tmp_path))
+    monkeypatch.setattr(build.os, "replace", lambda a, b: moved.append(b))
+    if torch_there:
+        monkeypatch.setattr(build, "_binding_flags", lambda: [])
+        with pytest.raises(RuntimeError, match="does not compile"):
+            build.build()
+    else:
+        monkeypatch.setitem(sys.modules, "torch", None)
+        assert build.build() == build.LIBRARY
+    assert moved == [build.LIBRARY, build.STREAM_LIBRARY]
+    assert sum("-shared" in cmd for cmd in ran) == 2
