@@ -7,14 +7,13 @@ argument's result, and an argument of size a in an exponential adds a few a u.
   silu(z)       relative (6 + 3 |z|) u
   softplus(d)   relative (12 + 3 |d|) u, with the rounding of d = dt + bias in it
   exp(v A)      relative |v A| (r + 43 u) + 4 u, r that of v; 40 u of it cover the
-                join of pieces, whose sums of up to 128 values of v are four chains
-                of at most 32, joined by 2 more additions
+                join of pieces of up to 128 rows, whose sums of v are four chains of
+                at most 32 values, joined by 3 more additions; for longer pieces the
+                caller of scan() names the length of the chains as `join`
   sums          n terms: n u times the sum of the magnitudes
 Every stored value adds half a step of its type, and where that is coarser half
 of the type's smallest subnormal.
 """
-import math
-
 import torch
 
 U = 2.0 ** -24
@@ -96,7 +95,7 @@ def conv(x, weight, bias, cu, state, slots, has, act):
 
 # ------------------------------------------------------------------------ scan
 
-def scan(x, dt, A, B, C, D, z, dt_bias, softplus, cu, state, slots, has):
+def scan(x, dt, A, B, C, D, z, dt_bias, softplus, cu, state, slots, has, join=40):
     """(out, bound, rows written, state, its bound, slots written)."""
     io, st = x.dtype, state.dtype
     x, dt, A, B, C, D, z, dt_bias = (f64(t) for t in (x, dt, A, B, C, D, z, dt_bias))
@@ -125,7 +124,7 @@ def scan(x, dt, A, B, C, D, z, dt_bias, softplus, cu, state, slots, has):
                 r_v = 2 * U * torch.ones_like(d)
             arg = v[:, None] * A
             e = torch.exp(arg)
-            r_e = arg.abs() * (r_v[:, None] + 43 * U) + 4 * U
+            r_e = arg.abs() * (r_v[:, None] + (3 + join) * U) + 4 * U
             u = (v * x[t])[:, None] * B[t].repeat_interleave(per, 0)
             e_s = e * e_s * (1 + r_e) + (e * s).abs() * (r_e + U) + u.abs() * (r_v[:, None] + 4 * U)
             s = e * s + u
@@ -186,7 +185,3 @@ def starts(lengths, first=0):
     for n in lengths:
         cu.append(cu[-1] + n)
     return cu
-
-
-def inverse_softplus(v):
-    return v + math.log(-math.expm1(-v))
