@@ -4,8 +4,8 @@ several ways by forking its slots, decoding, and compaction when requests end.
 
 The model is random: a few layers of projection, short convolution, selective scan
 (one decay per channel and state element) and projection, with residuals. The run checks
-itself: the tokens that the packed, forked and compacted run decodes are those of every
-request run alone from its first token on.
+itself: the scores that the packed, forked and compacted run gives the tokens are those of
+every request run alone from its first token on, but for bf16 roundings.
 
     python examples/state_space_serving.py [--layers 4] [--dim 512] [--tokens 24]
 """

@@ -4,7 +4,7 @@
  * ssd.h, with their conventions (device pointers owned by the caller, `stream` a
  * hipStream_t, an ssu_status returned, ssu_last_error() names what is wrong, no
  * allocation, no copy between host and device, no synchronisation: every call
- * may be recorded into a HIP graph).
+ * may be recorded into a HIP graph; the operands' GPU is the current one).
  *
  *   ssu_conv1d_varlen / ssu_conv1d_update  short causal depthwise convolution
  *   ssu_scan_varlen / ssu_scan_update      selective scan with one decay per
@@ -81,9 +81,9 @@ int ssu_conv1d_update(const ssu_conv_args *args, void *stream);
 typedef struct ssu_scan_args {
     uint32_t struct_size;      /* sizeof(ssu_scan_args) */
     int32_t state_dtype;       /* ssu_dtype */
-    void *state;               /* [nslots, dim, dstate], a slot's values dense */
+    void *state;               /* [nslots, dim, dstate], a slot's values dense; 16-byte aligned */
     int64_t nslots;            /* >= 1 */
-    int64_t slot_stride;       /* elements between slots, >= dim * dstate */
+    int64_t slot_stride;       /* elements between slots, >= dim * dstate, a multiple of 16 bytes */
     int64_t rows, dim, dstate, ngroups; /* dstate 8, 16, 32, 64, 128 or 256 */
     const void *x, *z, *dt;    /* [rows, dim]; z may be NULL (no gate) */
     const void *B, *C;         /* [rows, ngroups, dstate], groups dense in a row */
@@ -105,7 +105,8 @@ typedef struct ssu_scan_args {
     int32_t reserved;          /* 0 */
     int64_t pad_slot_id;
     void *workspace;           /* varlen: ssu_scan_workspace_bytes(...) bytes, 256-byte
-                                  aligned; may be NULL if that is 0 */
+                                  aligned; may be NULL if that is 0. One call at a time: its
+                                  kernels hand each other states through it */
     size_t workspace_bytes;
 } ssu_scan_args;
 

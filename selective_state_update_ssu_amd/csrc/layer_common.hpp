@@ -83,8 +83,9 @@ struct Raw<T, 1> {
 };
 
 // v * sigmoid(v) with the hardware's exp2 and reciprocal (each within about one
-// unit in the last place, far below one rounding of a 16-bit result; an fp32 result is
-// off by a few 2^-24 relative). Minus infinity gives NaN as the formula does.
+// unit in the last place). The exponent's argument is rounded, which grows with it: an fp32
+// result is off by up to (6 + 3 |v|) 2^-24 relative, far below one rounding of a 16-bit
+// result until sigmoid is 2^-126. Minus infinity gives NaN as the formula does.
 __device__ __forceinline__ float silu_fast(float v) {
     return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * v));
 }

@@ -121,9 +121,9 @@ struct Sequences {
 // it, which goes on past its own tile for them. Inputs are requested kBatch rows
 // ahead of their use, the first ones before the rows' sequences are known.
 //
-// Memory bounds long prompts: 17,885 rows of 10,240 channels in bf16 (733 MB) take 134 us, 5.5
-// TB/s, with tiles of 16 rows (150, 153 and 162 us with 8, 32 and 64) and outputs that
-// bypass the caches (146 us without; 149 us if the inputs bypass them too). Few rows are
+// Memory bounds long prompts: 17,885 rows of 10,240 channels in bf16 (733 MB) take 138 to 140 us,
+// 5.3 TB/s, with tiles of 16 rows (142, 149 and 157 us with 8, 32 and 64) and outputs that
+// bypass the caches (145 us without; 138 us if the inputs bypass them too). Few rows are
 // latency: tiles of 4 rows then put more waves on it.
 template <typename T, int VEC, int W>
 __global__ __launch_bounds__(kThreads) void conv_varlen_kernel(const ConvParams p) {

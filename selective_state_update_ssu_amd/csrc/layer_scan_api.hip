@@ -16,10 +16,12 @@ int64_t channel_blocks(int64_t dim, int64_t ngroups) {
 
 // Rows of a piece, or 0: with kEnough workgroups from the sequences alone, or none longer
 // than a piece, nothing is cut. Otherwise pieces are cut so that about kWanted come to be,
-// six per compute unit (1,280 to 2,560 lie within 3 %, 5,120 are 22 % slower for the joins).
-// Whole against cut, 5,120 channels x 16, sequences of 1,024 rows of mixed lengths: 143 against
-// 56 us with 80 workgroups (one sequence), 195 / 155 with 320, 186 / 191 with 400, 222 / 318
-// with 640; the two meet at about 400 to 480 workgroups for 1,024 channels and for a dstate of 64 too.
+// six per compute unit (1,280 to 2,560 lie within 3 %, 5,120 are 24 % slower for the joins).
+// Whole against cut, 5,120 channels x 16, sequences of 1,024 rows: 144 against 53 us with 80
+// workgroups (one sequence), 178 / 152 with 320, 181 / 175 with 400, 229 / 325 with 640; with
+// a dstate of 64 the two meet at about 320 workgroups, with 1,024 channels at 512. The rule
+// counts sequences, since their lengths are on the device: a long one beside
+// empty or short ones that make up the 400 is walked whole, at 0.14 us a row.
 constexpr int64_t kEnough = 400, kWanted = 1536, kShortest = 64;
 
 int64_t piece_rows(int64_t rows, int64_t nseq, int64_t blocks) {

@@ -16,7 +16,8 @@ loop: Python binding of include/layer.h.
 
 As in the decode step's binding, checks are host checks of shapes, dtypes, strides and
 devices; kernels run on the current stream (or `stream=`); nothing is copied to
-the host and nothing synchronises. The checks and the calls themselves are native
+the host and nothing synchronises. Calls that change one `refcount` are made by one
+thread at a time. The checks and the calls themselves are native
 (csrc/layer_binding.cpp): a decode step of a few sequences is 4 us on the GPU, less than
 filling its arguments from Python takes. There is no fallback: without the built library
 and binding every call raises.
@@ -113,7 +114,7 @@ def selective_scan_varlen(state, x, dt, A, B, C, cu_seqlens, out=None, *, D=None
 
     x, z and dt are [rows, dim] (dt fp32 or x's dtype), B and C [rows, groups, dstate], A
     fp32 [dim, dstate], D and dt_bias fp32 [dim]; rows of x, z, dt, B and C may be
-    strided. state [slots, dim, dstate] (fp32, fp16 or bf16) is read where
+    strided. state [slots, dim, dstate] (fp32, fp16 or bf16, its slots 16-byte aligned) is read where
     has_initial_state (None: nowhere) is true and holds each sequence's last state
     afterwards. Rows of no sequence, and those of one whose slot is pad_slot_id or out of
     range, are not written.
