@@ -374,7 +374,13 @@ ssu_cache_args counts(const Tensor& refcount) {
     return a;
 }
 
+// A tensor is a sequence of its slots, which are no caches.
+void check_list(PyObject* caches) {
+    if (THPVariable_Check(caches)) value_error("caches must be a list of tensors, got a tensor");
+}
+
 std::vector<ssu_cache_block> blocks(PyObject* caches, int64_t nslots, at::Device device) {
+    check_list(caches);
     PyObject* seq = PySequence_Fast(caches, "caches must be a list of tensors");
     if (!seq) throw Error{nullptr, ""};
     std::vector<ssu_cache_block> out;
@@ -436,6 +442,7 @@ PyObject* cache_adjust(PyObject* const* arg) {
 // (caches, src, dst)
 PyObject* cache_copy(PyObject* const* arg) {
     const Tensor &src = tensor("src", arg[1]), &dst = tensor("dst", arg[2]);
+    check_list(arg[0]);
     const Py_ssize_t n = PySequence_Size(arg[0]);
     if (n < 0) throw Error{nullptr, ""};
     if (n == 0) Py_RETURN_NONE;

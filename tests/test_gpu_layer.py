@@ -818,3 +818,14 @@ def test_allocation_errors_are_torchs():
         with pytest.raises(ValueError, match="n must be"):
             ssu.cache_alloc(count, n)
     assert count.tolist() == [0] * 4
+
+
+def test_a_tensor_is_no_list_of_caches():
+    cache = torch.arange(48, dtype=torch.float32, device=DEV).reshape(4, 4, 3)
+    before, ids = cache.clone(), torch.tensor([0], dtype=torch.int32, device=DEV)
+    count = torch.tensor([1, 0, 1, 0], dtype=torch.int32, device=DEV)
+    for call in (lambda: ssu.cache_copy(cache, ids, ids + 1), lambda: ssu.cache_fork(cache, count, ids),
+                 lambda: ssu.cache_compact(cache, count)):
+        with pytest.raises(ValueError, match="list of tensors"):
+            call()
+    assert same(cache, before) and count.tolist() == [1, 0, 1, 0]

@@ -380,3 +380,11 @@ def test_build_of_the_library_does_not_need_the_binding(torch_there, monkeypatch
         assert build.build() == build.LIBRARY
     assert moved == [build.LIBRARY, build.STREAM_LIBRARY]
     assert sum("-shared" in cmd for cmd in ran) == 2
+
+
+def test_binding_refuses_a_tensor_for_a_list_of_caches():
+    """A tensor is a sequence of its slots: taken as caches they would be copied inside."""
+    import torch
+    ids = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="list of tensors"):
+        ssu.cache_copy(torch.zeros(4, 4, 3), ids, ids)
