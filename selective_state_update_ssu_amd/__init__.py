@@ -24,6 +24,13 @@ kernel. There is no fallback: without the built library every call raises.
     selective_scan_update, cache_alloc, cache_free, cache_retain, cache_copy, cache_fork,
     cache_compact: the operators around the update (layer.py, include/layer.h)
 
+    linear_attention_varlen, linear_attention_update, linear_attention_packed: linear
+    attention with a decay per head, plain and with the delta rule (attention.py,
+    include/attention.h)
+
+    verify_drafts, batch_plan: drafted tokens and the tables of a packed batch (batch.py,
+    include/batch.h)
+
 Operand shapes follow the MATE documentation page "Source code for mate.mamba"
 (`selective_state_update`): state [slots, heads, dim, dstate]; x, z, out
 [rows, heads, dim]; dt [rows, heads], [rows, heads, 1] or [rows, heads, dim]
@@ -748,4 +755,10 @@ def ssd_combined_fwd_varlen(x, dt, A, B, C, chunk_size, cu_seqlens, cu_chunk_seq
 from . import layer  # noqa: E402
 from .layer import *  # noqa: E402,F401,F403
 
-__all__ += layer.__all__
+# ------------------------------------- linear attention, and between two model steps
+
+from . import attention, batch  # noqa: E402
+from .attention import *  # noqa: E402,F401,F403
+from .batch import *  # noqa: E402,F401,F403
+
+__all__ += layer.__all__ + attention.__all__ + batch.__all__

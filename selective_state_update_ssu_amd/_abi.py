@@ -1,4 +1,4 @@
-"""ctypes mirror of include/ssu.h, include/ssd.h and include/layer.h. Field order and types must match the header;
+"""ctypes mirror of the headers in include/. Field order and types must match the header;
 the library checks `struct_size` on every call, so a stale mirror fails loudly."""
 import ctypes
 import os
@@ -17,6 +17,11 @@ EXPORTS = ("ssu_one_token", "ssu_packed_varlen", "ssu_ring_update", "ssu_ring_co
 LAYER_EXPORTS = ("ssu_conv1d_varlen", "ssu_conv1d_update", "ssu_scan_workspace_bytes",
                  "ssu_scan_varlen", "ssu_scan_update", "ssu_cache_alloc", "ssu_cache_adjust",
                  "ssu_cache_copy", "ssu_cache_compact")
+
+# include/attention.h and include/batch.h
+ATTENTION_EXPORTS = ("ssu_attention_workspace_bytes", "ssu_attention_varlen",
+                     "ssu_attention_update", "ssu_attention_packed")
+BATCH_EXPORTS = ("ssu_verify_workspace_bytes", "ssu_verify_drafts", "ssu_batch_plan")
 
 
 class Operands(ctypes.Structure):
@@ -127,6 +132,54 @@ class CacheArgs(ctypes.Structure):
     ]
 
 
+class AttentionArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", c_uint32), ("state_dtype", c_int32),
+        ("state", c_void_p), ("nslots", c_int64), ("slot_stride", c_int64),
+        ("rows", c_int64), ("nheads", c_int64), ("ngroups", c_int64),
+        ("key_dim", c_int64), ("value_dim", c_int64),
+        ("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("out", c_void_p),
+        ("q_stride", c_int64), ("k_stride", c_int64), ("v_stride", c_int64),
+        ("out_stride", c_int64), ("io_dtype", c_int32), ("beta_dtype", c_int32),
+        ("decay", c_void_p), ("decay_stride", c_int64),
+        ("beta", c_void_p), ("beta_stride", c_int64), ("scale", c_double),
+        ("nseq", c_int64), ("cu_seqlens", c_void_p), ("cu_dtype", c_int32),
+        ("slot_dtype", c_int32), ("has_initial", c_void_p), ("slots", c_void_p),
+        ("slot_seq_stride", c_int64), ("slot_step_stride", c_int64),
+        ("num_accepted", c_void_p), ("dst", c_void_p),
+        ("dst_seq_stride", c_int64), ("dst_step_stride", c_int64),
+        ("dst_dtype", c_int32), ("reserved", c_int32), ("steps", c_int64),
+        ("pad_slot_id", c_int64), ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+    ]
+
+
+class VerifyArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", c_uint32), ("target_dtype", c_int32),
+        ("target", c_void_p), ("target_stride", c_int64), ("rows", c_int64), ("vocab", c_int64),
+        ("nseq", c_int64), ("window", c_int64), ("cu_seqlens", c_void_p), ("cu_dtype", c_int32),
+        ("draft_dtype", c_int32), ("drafts", c_void_p),
+        ("draft_seq_stride", c_int64), ("draft_step_stride", c_int64),
+        ("draft_probs", c_void_p), ("probs_seq_stride", c_int64), ("probs_step_stride", c_int64),
+        ("probs_dtype", c_int32), ("reserved", c_int32),
+        ("uniforms", c_void_p), ("uniform_stride", c_int64), ("temperature", c_void_p),
+        ("tokens", c_void_p), ("num_accepted", c_void_p),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+    ]
+
+
+class PlanArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", c_uint32), ("length_dtype", c_int32), ("lengths", c_void_p),
+        ("context", c_void_p), ("context_dtype", c_int32), ("table_dtype", c_int32),
+        ("nseq", c_int64), ("rows", c_int64), ("chunk_size", c_int64), ("nchunks", c_int64),
+        ("block_table", c_void_p), ("table_stride", c_int64), ("table_width", c_int64),
+        ("block_size", c_int64), ("cu_seqlens", c_void_p), ("row_seq", c_void_p),
+        ("row_pos", c_void_p), ("row_slots", c_void_p), ("cu_chunk_seqlens", c_void_p),
+        ("seq_idx", c_void_p), ("last_chunk_indices", c_void_p),
+    ]
+
+
 def load(path: str) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise RuntimeError(
@@ -149,11 +202,19 @@ def load(path: str) -> ctypes.CDLL:
     for f, args in ((lib.ssu_conv1d_varlen, ConvArgs), (lib.ssu_conv1d_update, ConvArgs),
                     (lib.ssu_scan_varlen, ScanArgs), (lib.ssu_scan_update, ScanArgs),
                     (lib.ssu_cache_alloc, CacheArgs), (lib.ssu_cache_adjust, CacheArgs),
-                    (lib.ssu_cache_copy, CacheArgs), (lib.ssu_cache_compact, CacheArgs)):
+                    (lib.ssu_cache_copy, CacheArgs), (lib.ssu_cache_compact, CacheArgs),
+                    (lib.ssu_attention_varlen, AttentionArgs),
+                    (lib.ssu_attention_update, AttentionArgs),
+                    (lib.ssu_attention_packed, AttentionArgs),
+                    (lib.ssu_verify_drafts, VerifyArgs), (lib.ssu_batch_plan, PlanArgs)):
         f.restype = c_int32
         f.argtypes = [ctypes.POINTER(args), c_void_p]
     lib.ssu_scan_workspace_bytes.restype = c_size_t
     lib.ssu_scan_workspace_bytes.argtypes = [c_int64] * 5
+    lib.ssu_attention_workspace_bytes.restype = c_size_t
+    lib.ssu_attention_workspace_bytes.argtypes = [c_int64] * 5 + [c_int32]
+    lib.ssu_verify_workspace_bytes.restype = c_size_t
+    lib.ssu_verify_workspace_bytes.argtypes = [c_int64] * 3 + [c_int32]
     lib.ssu_last_error.restype = c_char_p
     lib.ssu_last_error.argtypes = []
     lib.ssu_version.restype = c_int32

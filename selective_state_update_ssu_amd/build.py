@@ -1,8 +1,8 @@
 """Compile the HIP sources into the in-tree shared library `_lib/libssu_amd.so`.
 
 Every translation unit is compiled for gfx950 only, in parallel, then linked into
-one shared library that exports the C ABI of include/ssu.h, include/ssd.h and
-include/layer.h. Packed-fp32 VALU instructions are disabled for the device code.
+one shared library that exports the C ABI of the headers in include/. Packed-fp32 VALU
+instructions are disabled for the device code.
 """
 from __future__ import annotations
 
@@ -23,9 +23,13 @@ LIBRARY = os.path.join(LIB_DIR, "libssu_amd.so")
 STREAM_LIBRARY = os.path.join(LIB_DIR, "libssu_stream.so")
 STREAM_SOURCES = ["stream_ceiling.hip"]
 
-# Python side of include/layer.h: host code against torch's headers, linked to the library.
+# Python side of include/layer.h, and of include/attention.h and include/batch.h: host code
+# against torch's headers, linked to the library.
 BINDING = os.path.join(LIB_DIR, "_layer_binding.so")
 BINDING_SOURCE = "layer_binding.cpp"
+SERVE_BINDING = os.path.join(LIB_DIR, "_serve_binding.so")
+SERVE_BINDING_SOURCE = "serve_binding.cpp"
+BINDINGS = ((BINDING, BINDING_SOURCE), (SERVE_BINDING, SERVE_BINDING_SOURCE))
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CXX = os.environ.get("HIP_CXX", "/opt/rocm/llvm/bin/clang++")
@@ -33,7 +37,10 @@ ARCH = "gfx950"
 SOURCES = ["ssu_api.hip", "ssu_kernels_f32.hip", "ssu_kernels_f16.hip", "ssu_kernels_bf16.hip",
            "ring_trackers.hip", "ssd_api.hip", "ssd_kernels_bf16.hip", "ssd_kernels_f16.hip",
            "layer_conv.hip", "layer_scan_api.hip", "layer_scan_f32.hip", "layer_scan_f16.hip",
-           "layer_scan_bf16.hip", "layer_cache.hip"]
+           "layer_scan_bf16.hip", "layer_cache.hip", "attention_api.hip",
+           "attention_step_f32.hip", "attention_step_f16.hip", "attention_step_bf16.hip",
+           "attention_chunk_f32.hip", "attention_chunk_f16.hip", "attention_chunk_bf16.hip",
+           "batch_verify.hip", "batch_plan.hip"]
 CXXFLAGS = [
     f"--offload-arch={ARCH}",
     "-O3",
@@ -75,18 +82,18 @@ def _compile(cmd, src):
     return obj, _run([*cmd, "-c", os.path.join(CSRC, src), "-o", obj])
 
 
-def _link_binding(obj):
+def _link_binding(binding, obj):
     import torch
     torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    _run([CXX, "-shared", "-fPIC", "-o", BINDING + ".tmp", obj,
+    _run([CXX, "-shared", "-fPIC", "-o", binding + ".tmp", obj,
           f"-L{LIB_DIR}", "-l:" + os.path.basename(LIBRARY), "-Wl,-rpath,$ORIGIN",
           f"-L{torch_lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"])
-    os.replace(BINDING + ".tmp", BINDING)
+    os.replace(binding + ".tmp", binding)
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source and link the library; returns its path. The Python binding comes
-    after it and needs torch and its headers: without torch the library is built alone."""
+    """Compile every source and link the library; returns its path. The Python bindings come
+    after it and need torch and its headers: without torch the library is built alone."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
     sources = SOURCES + STREAM_SOURCES
@@ -94,11 +101,12 @@ def build(verbose: bool = False) -> str:
         import torch  # noqa: F401
     except ImportError:
         torch = None
-    with ThreadPoolExecutor(max_workers=min(len(sources) + 1, os.cpu_count() or 1)) as ex:
+    workers = min(len(sources) + len(BINDINGS), os.cpu_count() or 1)
+    with ThreadPoolExecutor(max_workers=workers) as ex:
         jobs = {s: ex.submit(_compile, [HIPCC, *CXXFLAGS], s) for s in sources}
         if torch is not None:
-            jobs[BINDING_SOURCE] = ex.submit(lambda: _compile([CXX, *_binding_flags()],
-                                                              BINDING_SOURCE))
+            for _, source in BINDINGS:
+                jobs[source] = ex.submit(lambda s: _compile([CXX, *_binding_flags()], s), source)
     objs = {s: jobs[s].result() for s in sources}
     for lib, srcs in ((LIBRARY, SOURCES), (STREAM_LIBRARY, STREAM_SOURCES)):
         tmp = lib + ".tmp"
@@ -106,10 +114,11 @@ def build(verbose: bool = False) -> str:
               *[objs[s][0] for s in srcs]])
         os.replace(tmp, lib)
     if torch is not None:
-        objs[BINDING_SOURCE] = jobs[BINDING_SOURCE].result()
-        _link_binding(objs[BINDING_SOURCE][0])
+        for binding, source in BINDINGS:
+            objs[source] = jobs[source].result()
+            _link_binding(binding, objs[source][0])
     else:
-        print(f"torch is not importable: {BINDING} is not built", file=sys.stderr)
+        print(f"torch is not importable: {', '.join(b for b, _ in BINDINGS)} are not built", file=sys.stderr)
     for _, msg in objs.values():
         if msg and verbose:
             print(msg, file=sys.stderr)

@@ -1,0 +1,234 @@
+// attention_api.hip -- the entry points of linear attention (include/attention.h): checks of
+// the argument struct, the launches.
+#include "attention_common.hpp"
+
+namespace {
+
+using namespace attention;
+using layer::Rows;
+using layer::aligned;
+using layer::is_dtype;
+using layer::is_index;
+using layer::overlap;
+using layer::size_of;
+
+enum Entry { kVarlen, kUpdate, kPacked };
+
+int64_t index_size(int32_t d) { return d == SSU_I64 ? 8 : 4; }
+
+int check(const ssu_attention_args* a, Entry entry) {
+    using ssu::report;
+    constexpr int kBad = SSU_ERR_INVALID_ARGUMENT;
+    if (!a) return report(kBad, "args must not be NULL");
+    if (a->struct_size != sizeof(ssu_attention_args))
+        return report(kBad, "struct_size %u != sizeof(ssu_attention_args) %zu (header mismatch)",
+                      a->struct_size, sizeof(ssu_attention_args));
+    if (a->reserved != 0) return report(kBad, "reserved must be 0");
+    if (!is_dtype(a->state_dtype) || !is_dtype(a->io_dtype))
+        return report(kBad, "state_dtype %d or io_dtype %d is not an ssu_dtype", a->state_dtype,
+                      a->io_dtype);
+    if (a->beta && a->beta_dtype != SSU_F32 && a->beta_dtype != a->io_dtype)
+        return report(kBad, "beta must be fp32 or share the io dtype");
+    if (a->rows < 0 || a->nheads < 1 || a->ngroups < 1 || a->key_dim < 1 || a->value_dim < 1 ||
+        a->nslots < 1 || a->nseq < 0)
+        return report(kBad,
+                      "sizes must be positive (rows %lld, nheads %lld, ngroups %lld, key_dim %lld, "
+                      "value_dim %lld, nslots %lld, nseq %lld)",
+                      (long long)a->rows, (long long)a->nheads, (long long)a->ngroups,
+                      (long long)a->key_dim, (long long)a->value_dim, (long long)a->nslots,
+                      (long long)a->nseq);
+    if (a->nheads % a->ngroups)
+        return report(kBad, "nheads %lld must be a multiple of ngroups %lld",
+                      (long long)a->nheads, (long long)a->ngroups);
+    if (a->key_dim % 8 || a->key_dim > 256 || a->value_dim > 256)
+        return report(SSU_ERR_UNSUPPORTED,
+                      "key_dim %lld is not built (8 to 256 in steps of 8), or value_dim %lld (1 to "
+                      "256)", (long long)a->key_dim, (long long)a->value_dim);
+    if (a->rows > (1 << 30) || a->nseq > (1 << 30) || a->nheads > (1 << 20))
+        return report(SSU_ERR_UNSUPPORTED,
+                      "rows and nseq must be at most 2^30 and nheads at most 2^20");
+    const int64_t slot = a->nheads * a->value_dim * a->key_dim;
+    const int64_t qk = a->ngroups * a->key_dim, vo = a->nheads * a->value_dim;
+    if (a->slot_stride < slot)
+        return report(kBad, "slot_stride must be at least nheads * value_dim * key_dim");
+    if (a->q_stride < 0 || a->k_stride < 0 || a->v_stride < 0 || a->decay_stride < 0 ||
+        a->beta_stride < 0 || a->out_stride < vo)
+        return report(kBad,
+                      "strides must be >= 0 and out_stride at least nheads * value_dim");
+    if (entry != kUpdate && !is_index(a->cu_dtype))
+        return report(kBad, "cu_dtype %d is not an ssu_index_dtype", a->cu_dtype);
+    if (a->slots && !is_index(a->slot_dtype))
+        return report(kBad, "slot_dtype %d is not an ssu_index_dtype", a->slot_dtype);
+    if (entry == kUpdate && (a->cu_seqlens || a->nseq != a->rows))
+        return report(kBad, "an update has no cu_seqlens, and nseq must equal rows");
+    if (entry != kVarlen && (a->has_initial || a->workspace || a->workspace_bytes))
+        return report(kBad, "has_initial and workspace belong to ssu_attention_varlen");
+    if (entry != kPacked && (a->num_accepted || a->dst || a->steps))
+        return report(kBad, "num_accepted, dst and steps belong to ssu_attention_packed");
+    if (entry == kPacked) {
+        if (a->num_accepted && !a->slots)
+            return report(kBad, "num_accepted needs a slot table");
+        if (a->dst && !is_index(a->dst_dtype))
+            return report(kBad, "dst_dtype %d is not an ssu_index_dtype", a->dst_dtype);
+        if (a->slot_seq_stride < 0 || a->slot_step_stride < 0 || a->dst_seq_stride < 0 ||
+            a->dst_step_stride < 0)
+            return report(kBad, "table strides must be >= 0");
+        if ((a->num_accepted || a->dst) && a->steps < 1)
+            return report(kBad, "steps must be >= 1 with num_accepted or dst");
+    }
+    if (a->rows == 0 || a->nseq == 0) return SSU_OK;
+    const int64_t io = size_of(a->io_dtype), st = size_of(a->state_dtype),
+                  be = size_of(a->beta_dtype), cu = index_size(a->cu_dtype);
+    const int64_t steps = a->steps > 0 ? a->steps : 1;
+    const auto table = [&](const void* t, int64_t seq, int64_t step, int32_t dtype) {
+        return Rows(t, ((a->nseq - 1) * seq + (steps - 1) * step + 1) * index_size(dtype));
+    };
+    const Rows slots = entry == kPacked
+                           ? table(a->slots, a->slot_seq_stride, a->slot_step_stride, a->slot_dtype)
+                           : Rows(a->slots, a->nseq * index_size(a->slot_dtype));
+    const struct { const char* name; int64_t align; Rows rows; bool optional; } in[] = {
+        {"q", io, Rows(a->q, a->rows, a->q_stride, qk, io), false},
+        {"k", io, Rows(a->k, a->rows, a->k_stride, qk, io), false},
+        {"v", io, Rows(a->v, a->rows, a->v_stride, vo, io), false},
+        {"decay", 4, Rows(a->decay, a->rows, a->decay_stride, a->nheads, 4), false},
+        {"beta", be, Rows(a->beta, a->rows, a->beta_stride, a->nheads, be), true},
+        {"cu_seqlens", cu, Rows(a->cu_seqlens, (a->nseq + 1) * cu), entry == kUpdate},
+        {"has_initial", 1, Rows(a->has_initial, a->nseq), true},
+        {"slots", index_size(a->slot_dtype), slots, true},
+        {"num_accepted", cu, Rows(a->num_accepted, a->nseq * cu), true},
+        {"dst", index_size(a->dst_dtype),
+         table(a->dst, a->dst_seq_stride, a->dst_step_stride, a->dst_dtype), true},
+    };
+    if (!a->state) return report(kBad, "state must not be NULL");
+    if (!a->out) return report(kBad, "out must not be NULL");
+    for (const auto& x : in) {
+        if (!x.rows.p && !x.optional) return report(kBad, "%s must not be NULL", x.name);
+        if (!aligned(x.rows.p, x.align))
+            return report(kBad, "%s must be aligned to its dtype", x.name);
+    }
+    if (!aligned(a->out, io)) return report(kBad, "out must be aligned to its dtype");
+    if (!aligned(a->state, 16) || a->slot_stride * st % 16)
+        return report(SSU_ERR_UNSUPPORTED, "state and its slots must be 16-byte aligned");
+    int64_t ws = 0;
+    if (entry == kVarlen) {
+        ws = static_cast<int64_t>(ssu_attention_workspace_bytes(
+            a->rows, a->nseq, a->nheads, a->key_dim, a->value_dim, a->beta != nullptr));
+        if (ws > 0 && (!a->workspace || !aligned(a->workspace, 256) ||
+                       a->workspace_bytes < static_cast<size_t>(ws)))
+            return report(kBad, "workspace must be 256-byte aligned and hold %lld bytes (got %zu)",
+                          (long long)ws, a->workspace_bytes);
+    }
+    const struct { const char* name; Rows rows; } written[] = {
+        {"out", Rows(a->out, a->rows, a->out_stride, vo, io)},
+        {"state", Rows(a->state, a->nslots, a->slot_stride, slot, st)},
+        {"workspace", Rows(a->workspace, ws)}};
+    for (int i = 0; i < 3; ++i) {
+        for (const auto& x : in)
+            if (overlap(written[i].rows, x.rows))
+                return report(kBad, "%s overlaps %s", written[i].name, x.name);
+        for (int j = 0; j < i; ++j)
+            if (overlap(written[i].rows, written[j].rows))
+                return report(kBad, "%s overlaps %s", written[i].name, written[j].name);
+    }
+    return SSU_OK;
+}
+
+Params params(const ssu_attention_args* a) {
+    Params p{};
+    p.state = a->state;
+    p.q = a->q;
+    p.k = a->k;
+    p.v = a->v;
+    p.out = a->out;
+    p.decay = a->decay;
+    p.beta = a->beta;
+    p.cu = a->cu_seqlens;
+    p.has = a->has_initial;
+    p.slots = a->slots;
+    p.na = a->num_accepted;
+    p.dst = a->dst;
+    p.nslots = a->nslots;
+    p.slot_stride = a->slot_stride;
+    p.rows = a->rows;
+    p.nseq = a->nseq;
+    p.pad_slot_id = a->pad_slot_id;
+    p.q_stride = a->q_stride;
+    p.k_stride = a->k_stride;
+    p.v_stride = a->v_stride;
+    p.out_stride = a->out_stride;
+    p.decay_stride = a->decay_stride;
+    p.beta_stride = a->beta_stride;
+    p.slot_seq_stride = a->slot_seq_stride;
+    p.slot_step_stride = a->slot_step_stride;
+    p.dst_seq_stride = a->dst_seq_stride;
+    p.dst_step_stride = a->dst_step_stride;
+    p.steps = a->steps;
+    p.scale = static_cast<float>(a->scale);
+    p.nheads = static_cast<int32_t>(a->nheads);
+    p.ngroups = static_cast<int32_t>(a->ngroups);
+    p.per_group = p.nheads / p.ngroups;
+    p.K = static_cast<int32_t>(a->key_dim);
+    p.V = static_cast<int32_t>(a->value_dim);
+    p.state_dtype = a->state_dtype;
+    p.beta_f32 = a->beta_dtype == SSU_F32;
+    p.cu64 = a->cu_dtype == SSU_I64;
+    p.slot64 = a->slot_dtype == SSU_I64;
+    p.dst64 = a->dst_dtype == SSU_I64;
+    const int64_t io = size_of(a->io_dtype);
+    const auto wide = [&](const void* base, int64_t stride, int64_t dim, int64_t bytes) {
+        return aligned(base, bytes) && stride * io % bytes == 0 && dim * io % bytes == 0;
+    };
+    p.wide = (wide(a->q, a->q_stride, a->key_dim, 16) && wide(a->k, a->k_stride, a->key_dim, 16)) |
+             (wide(a->v, a->v_stride, a->value_dim, 16) && a->value_dim % 8 == 0) << 1;
+    p.wide_out = wide(a->out, a->out_stride, a->value_dim, 4 * io);
+    return p;
+}
+
+int outcome(hipError_t e, const char* entry) {
+    if (e == hipErrorInvalidConfiguration)
+        return ssu::report(SSU_ERR_UNSUPPORTED, "%s: too many sequences and heads for one call",
+                           entry);
+    if (e != hipSuccess)
+        return ssu::report(SSU_ERR_LAUNCH, "%s: launch failed: %s", entry, hipGetErrorString(e));
+    return ssu::report_ok();
+}
+
+int step(const ssu_attention_args* a, bool packed, void* stream, const char* entry) {
+    if (int rc = check(a, packed ? kPacked : kUpdate)) return rc;
+    if (a->rows == 0 || a->nseq == 0) return ssu::report_ok();
+    const Params p = params(a);
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    return outcome(a->io_dtype == SSU_F32   ? step_f32(p, packed, st)
+                   : a->io_dtype == SSU_F16 ? step_f16(p, packed, st)
+                                            : step_bf16(p, packed, st),
+                   entry);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssu_attention_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int32_t) {
+    return 0;
+}
+
+int ssu_attention_varlen(const ssu_attention_args* a, void* stream) {
+    if (int rc = check(a, kVarlen)) return rc;
+    if (a->rows == 0 || a->nseq == 0) return ssu::report_ok();
+    const Params p = params(a);
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    return outcome(a->io_dtype == SSU_F32   ? chunk_f32(p, st)
+                   : a->io_dtype == SSU_F16 ? chunk_f16(p, st)
+                                            : chunk_bf16(p, st),
+                   "ssu_attention_varlen");
+}
+
+int ssu_attention_update(const ssu_attention_args* a, void* stream) {
+    return step(a, false, stream, "ssu_attention_update");
+}
+
+int ssu_attention_packed(const ssu_attention_args* a, void* stream) {
+    return step(a, true, stream, "ssu_attention_packed");
+}
+
+}  // extern "C"
