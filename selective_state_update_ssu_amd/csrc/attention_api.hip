@@ -12,6 +12,35 @@ using layer::is_index;
 using layer::overlap;
 using layer::size_of;
 
+constexpr int64_t kAlign = 256;
+int64_t round_up(int64_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+
+// How a call's sequences are cut, and its scratch.
+constexpr int64_t kWanted = 1024, kShortest = 256;
+
+struct Plan {
+    int64_t piece, pieces, ends, sums, moves, total;
+};
+
+Plan plan_of(int64_t rows, int64_t nseq, int64_t nheads, int64_t K, int64_t V, bool delta) {
+    Plan o{};
+    const int64_t each = nheads * ((V + 63) / 64);
+    o.pieces = nseq;
+    if (nseq * each < kWanted / 2 && rows > 0) {
+        int64_t piece = (rows * each + kWanted - 1) / kWanted;
+        piece = (piece < kShortest ? kShortest : piece + 63) / 64 * 64;
+        if (piece < rows) {
+            o.piece = piece;
+            o.pieces = rows / piece + nseq;
+            o.sums = o.ends + round_up(o.pieces * nheads * V * K * 4);
+            o.moves = o.sums;
+            o.total = delta ? o.moves + round_up(o.pieces * nheads * K * K * 4)
+                            : o.sums + round_up(o.pieces * nheads * 4);
+        }
+    }
+    return o;
+}
+
 enum Entry { kVarlen, kUpdate, kPacked };
 
 int64_t index_size(int32_t d) { return d == SSU_I64 ? 8 : 4; }
@@ -175,12 +204,18 @@ Params params(const ssu_attention_args* a) {
     p.slot64 = a->slot_dtype == SSU_I64;
     p.dst64 = a->dst_dtype == SSU_I64;
     const int64_t io = size_of(a->io_dtype);
-    const auto wide = [&](const void* base, int64_t stride, int64_t dim, int64_t bytes) {
-        return aligned(base, bytes) && stride * io % bytes == 0 && dim * io % bytes == 0;
+    // Rows of every head aligned to 16 bytes, none inside another.
+    const auto wide = [&](const void* base, int64_t stride, int64_t heads, int64_t dim) {
+        return aligned(base, 16) && stride * io % 16 == 0 && dim * io % 16 == 0 &&
+               (a->rows <= 1 || stride >= heads * dim);
     };
-    p.wide = (wide(a->q, a->q_stride, a->key_dim, 16) && wide(a->k, a->k_stride, a->key_dim, 16)) |
-             (wide(a->v, a->v_stride, a->value_dim, 16) && a->value_dim % 8 == 0) << 1;
-    p.wide_out = wide(a->out, a->out_stride, a->value_dim, 4 * io);
+    const auto near = [&](int64_t stride) { return stride < (int64_t(1) << 30) / (64 * io); };
+    p.wide_qk = wide(a->q, a->q_stride, a->ngroups, a->key_dim) &&
+                wide(a->k, a->k_stride, a->ngroups, a->key_dim);
+    p.wide = p.wide_qk && a->rows > 1 && a->value_dim % 8 == 0 &&
+             wide(a->v, a->v_stride, a->nheads, a->value_dim) &&
+             wide(a->out, a->out_stride, a->nheads, a->value_dim) && near(a->q_stride) &&
+             near(a->k_stride) && near(a->v_stride) && near(a->out_stride);
     return p;
 }
 
@@ -208,14 +243,23 @@ int step(const ssu_attention_args* a, bool packed, void* stream, const char* ent
 
 extern "C" {
 
-size_t ssu_attention_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int32_t) {
-    return 0;
+size_t ssu_attention_workspace_bytes(int64_t rows, int64_t nseq, int64_t nheads, int64_t key_dim,
+                                     int64_t value_dim, int32_t delta) {
+    if (rows < 0 || nseq < 0 || nheads < 1 || key_dim < 1 || value_dim < 1) return 0;
+    return static_cast<size_t>(plan_of(rows, nseq, nheads, key_dim, value_dim, delta != 0).total);
 }
 
 int ssu_attention_varlen(const ssu_attention_args* a, void* stream) {
     if (int rc = check(a, kVarlen)) return rc;
     if (a->rows == 0 || a->nseq == 0) return ssu::report_ok();
-    const Params p = params(a);
+    Params p = params(a);
+    const Plan o = plan_of(a->rows, a->nseq, a->nheads, a->key_dim, a->value_dim, a->beta != nullptr);
+    char* ws = static_cast<char*>(a->workspace);
+    p.piece = o.piece;
+    p.pieces = o.pieces;
+    p.ends = reinterpret_cast<float*>(ws + o.ends);
+    p.sums = reinterpret_cast<float*>(ws + o.sums);
+    p.moves = reinterpret_cast<float*>(ws + o.moves);
     const hipStream_t st = static_cast<hipStream_t>(stream);
     return outcome(a->io_dtype == SSU_F32   ? chunk_f32(p, st)
                    : a->io_dtype == SSU_F16 ? chunk_f16(p, st)

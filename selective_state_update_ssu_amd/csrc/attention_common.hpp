@@ -33,16 +33,19 @@ struct Params {
     int64_t q_stride, k_stride, v_stride, out_stride, decay_stride, beta_stride;
     int64_t slot_seq_stride, slot_step_stride, dst_seq_stride, dst_step_stride, steps;
     // varlen: rows of a piece (0: every sequence is one piece), pieces of a call at most, and
-    // the states and decays that the passes hand each other.
+    // what the passes hand each other: [pieces, heads, value, key] states, [pieces, heads] decays or
+    // [pieces, heads, key, key] transitions.
     int64_t piece, pieces;
     float* ends;
     float* sums;
+    float* moves;
     float scale;
     int32_t nheads, ngroups, per_group, K, V;
     int32_t state_dtype, beta_f32, cu64, slot64, dst64;
-    int32_t wide;      // q, k and v rows of every head 16-byte aligned
-    int32_t wide_out;  // out rows of every head 8-byte aligned (fp32: 16)
-    int32_t blocks;    // workgroups along V
+    int32_t wide_qk;   // q and k rows of every head 16-byte aligned
+    int32_t wide;      // v and out rows too, and 64 rows of each span less than 2^31 bytes
+    int32_t blocks;    // workgroups along V (and the identity's columns)
+    int32_t value_blocks;
 };
 
 constexpr float kLog2e = layer::kLog2e;
@@ -58,10 +61,31 @@ __device__ __forceinline__ int64_t slot_at(const void* table, int is64, int64_t 
     return s == p.pad_slot_id || s < 0 || s >= p.nslots ? -1 : s;
 }
 
-__device__ __forceinline__ float state_load(const void* p, int dtype, int64_t i) {
-    if (dtype == SSU_F32) return static_cast<const float*>(p)[i];
-    if (dtype == SSU_F16) return static_cast<float>(static_cast<const _Float16*>(p)[i]);
-    return static_cast<float>(static_cast<const __bf16*>(p)[i]);
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// Four consecutive elements of a state at element i (a multiple of 4).
+template <typename ST>
+__device__ __forceinline__ f32x4 load4(const void* p, int64_t i) {
+    float f[4];
+    Raw<ST, 4>::widen(Raw<ST, 4>::load(static_cast<const ST*>(p) + i), f);
+    return f32x4{f[0], f[1], f[2], f[3]};
+}
+template <typename ST>
+__device__ __forceinline__ void store4(void* p, int64_t i, f32x4 v) {
+    const float f[4] = {v[0], v[1], v[2], v[3]};
+    Raw<ST, 4>::store(static_cast<ST*>(p) + i, Raw<ST, 4>::narrow(f));
+}
+__device__ __forceinline__ f32x4 state_load4(const void* p, int dtype, int64_t i) {
+    return dtype == SSU_F32 ? load4<float>(p, i)
+           : dtype == SSU_F16 ? load4<_Float16>(p, i) : load4<__bf16>(p, i);
+}
+__device__ __forceinline__ void state_store4(void* p, int dtype, int64_t i, f32x4 v) {
+    if (dtype == SSU_F32)
+        store4<float>(p, i, v);
+    else if (dtype == SSU_F16)
+        store4<_Float16>(p, i, v);
+    else
+        store4<__bf16>(p, i, v);
 }
 
 // Launchers of one io type's kernels, each in a translation unit of its own.

@@ -114,8 +114,8 @@ __global__ __launch_bounds__(kStepThreads) void step_kernel(const Params p) {
     for (int64_t t = begin; t < end; ++t) {
         float qf[VEC], kf[VEC];
         bits v_in[LOADS];
-        Piece<IT, VEC>::load(q + t * p.q_stride, p.wide, qf);
-        Piece<IT, VEC>::load(k + t * p.k_stride, p.wide, kf);
+        Piece<IT, VEC>::load(q + t * p.q_stride, p.wide_qk, qf);
+        Piece<IT, VEC>::load(k + t * p.k_stride, p.wide_qk, kf);
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) v_in[i] = v[t * p.v_stride + row[i]];
         const float e =

@@ -7,13 +7,14 @@ a state row: N <- e^g N + |r| |k| (2-norms of key vectors, exact r). One row's a
 by at most c u times its magnitudes, where c counts what is summed and rounded on the way: key_dim
 terms of a product with the state, up to 64 rows of a chunk twice (scores, values), 16 terms of a
 diagonal block's inverse against right-hand sides of up to beta (|v| + |k| N), and a few single
-roundings (the parts of a product leave out less than 2 u of it): c = key_dim + 200. An
+roundings (the parts of a product leave out less than 2 u of it): c = key_dim + 200. What reaches
+only a 16-bit out goes in as two parts of 8 bits, which leaves out 2^-17 of either factor: 256 u. An
 exponential of a sum x of decays is off by 3 |x| u relative, |x| at most the decays of 64 rows, and
 no more than 88 of them before it is 0 in fp32. The errors E of a state row (2-norm)
 come forward through e^g (1 - beta k k^T), whose norm is at most e^g where beta |k|^2 lies in
 [0, 2], so that
     E <- e^g E + c u (e^g N + |r| |k| + beta |k| (|v| + |k| N))
-    out: scale |q| (E + c u N), half a step of its type on top.
+    out: scale |q| (E + (c + 256 for 16 bits) u N), half a step of its type on top.
 """
 import torch
 
@@ -38,6 +39,7 @@ def attention(q, k, v, decay, beta, scale, cu, state, begin_of, end_of, has=None
     rows, H, V = v.shape
     per, K = H // q.shape[1], q.shape[2]
     g = decay.expand(rows, H).clamp(min=-300.0)
+    more = 0.0 if io == torch.float32 else 256 * U
     state = f64(state).clone()
     before = state.clone()
     s_bound = torch.zeros_like(state)
@@ -65,7 +67,7 @@ def attention(q, k, v, decay, beta, scale, cu, state, begin_of, end_of, has=None
             E = e * E + c * local
             N = e * N + r.abs() * kn
             y = scale * (S * qt[:, None]).sum(-1)
-            out[t], bound[t] = y, stored(abs(scale) * qn * (E + c * N), y, io)
+            out[t], bound[t] = y, stored(abs(scale) * qn * (E + (c + more) * N), y, io)
             written[t] = True
             to = end_of(b, t - begin, t + 1 == end)
             if to is not None:

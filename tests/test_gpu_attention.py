@@ -152,6 +152,31 @@ def test_prompts_bad_ranges_are_inert():
         prompts(c)
 
 
+@pytest.mark.parametrize("delta", [False, True])
+@pytest.mark.parametrize("lengths,H,G,K,V,io,st", [
+    ([1500], 2, 1, 64, 40, BF16, F32), ([900, 0, 257, 1, 700], 2, 2, 128, 72, F16, F32),
+    ([1100], 1, 1, 256, 256, BF16, BF16), ([300, 1030], 1, 1, 200, 30, F32, F32)])
+def test_prompts_cut_into_pieces(delta, lengths, H, G, K, V, io, st):
+    """Few heads: sequences of more than 256 rows are cut. Sequences of one, two, three and more
+    pieces, ends on a piece's end and one row behind it, inert slots among them."""
+    c = inputs(len(lengths) + K, lengths, H, G, K, V, io, st, delta, lead=1, tail=2,
+               inert=(1,) if len(lengths) > 2 else ())
+    assert ssu.attention_workspace_bytes(c["v"].shape[0], len(lengths), H, K, V, delta) > 255
+    prompts(c)
+
+
+def test_prompts_workspace():
+    c = inputs(30, [700, 400], 2, 1, 64, 64, BF16, F32, True)
+    cu = torch.tensor(c["cu"], dtype=torch.int32, device=DEV)
+    n = ssu.attention_workspace_bytes(1100, 2, 2, 64, 64, True)
+    a = run(c, ssu.linear_attention_varlen, cu_seqlens=cu)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device=DEV)
+    b = run(c, ssu.linear_attention_varlen, cu_seqlens=cu, workspace=ws)
+    assert same(a[0], b[0]) and same(a[1], b[1])
+    with pytest.raises(ValueError, match="workspace"):
+        run(c, ssu.linear_attention_varlen, cu_seqlens=cu, workspace=ws[:-1])
+
+
 def steps(c):
     out, state = run(c, ssu.linear_attention_update, state_batch_indices=c["slots"].to(DEV))
     rows = c["v"].shape[0]
@@ -252,7 +277,7 @@ def test_prompt_then_tokens_is_one_prompt():
 
 @pytest.mark.parametrize("entry", ["prompts", "step"])
 def test_captured_calls_follow_their_inputs(entry):
-    c = inputs(12, [40, 100, 3] if entry == "prompts" else [1] * 6, 4, 2, 64, 64, BF16, F32, True)
+    c = inputs(12, [40, 600, 3] if entry == "prompts" else [1] * 6, 4, 2, 64, 64, BF16, F32, True)
     args = [c[x].to(DEV).contiguous() for x in ("q", "k", "v", "decay")]
     beta, slots = c["beta"].to(DEV), c["slots"].to(DEV)
     cu = torch.tensor(c["cu"], dtype=torch.int32, device=DEV)
