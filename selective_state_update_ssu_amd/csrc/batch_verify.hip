@@ -1,11 +1,12 @@
 // batch_verify.hip -- verification of drafted tokens (semantics in include/batch.h).
 //
-// Three launches: (scores only) the largest score, the sum of exponentials and the first
-// largest token per part of each row; per sequence and tile of the vocabulary the number of
-// accepted drafts and the sum of the tile's weights; per sequence the tile in which the
-// drawn number falls, and the token. Rows are read once, the tile twice. Memory bounds the first
-// two, latency the last. Sums of weights are fp64, so that a drawn number next to a border
-// falls on the side on which the definition has it; their order is fixed.
+// From scores a first launch takes, per tile of every row, the largest score and the sum of
+// exponentials (of greedy rows the first largest token). A second one sums, per tile of the row
+// that a token is drawn from, its weights, and a third finds the tile in which the drawn number falls
+// and the token in it. Rows are read once, but for the one that a token is drawn from. Sums of
+// weights are fp64, so that a drawn number next to a border falls on the side on which the
+// definition has it; their order is fixed. (One workgroup per sequence for the second and third
+// launch: 84 us instead of 30 for 128 sequences of 131,072 tokens, and no faster for four.)
 #include "batch.h"
 #include "layer_common.hpp"
 
@@ -13,8 +14,8 @@ namespace {
 
 using namespace layer;
 
-constexpr int kThreads = 256, kWaves = kThreads / 64;
-constexpr int kSegs = 4;  // 16-byte segments of a thread in a tile
+constexpr int kThreads = 256, kWaves = kThreads / 64;   // of a tile's statistics
+constexpr int kSegs = 4;                                // 16-byte segments of a thread in a tile
 
 template <typename T>
 __host__ __device__ constexpr int seg_elements() { return 16 / static_cast<int>(sizeof(T)); }
@@ -28,9 +29,21 @@ __host__ inline int64_t tiles_of(int64_t vocab, int64_t size) {
 }
 
 struct Stats {   // of a tile of a row
-    float most;  // largest score
-    int first;   // and the first token that has it, INT_MAX if there is none
-    double sum;  // of exp((score - most) / temperature)
+    float most;  // largest score, minus infinity if there is none
+    int first;   // greedy: the first token that has it, INT_MAX if there is none
+    double sum;  // else: of exp((score - most) / temperature)
+};
+
+struct Row {  // what is known of a row before its weights are read
+    float most, temperature;
+    int first;
+    double c, inverse;  // log2(e) / temperature, 1 / sum of exponentials
+};
+
+struct Choice {  // of a sequence
+    int accepted, rejected;
+    int64_t draft;  // the rejected one
+    Row row;
 };
 
 struct VerifyParams {
@@ -43,7 +56,8 @@ struct VerifyParams {
     int32_t* tokens;
     int32_t* num_accepted;
     Stats* stats;   // [rows, tiles]
-    double* sums;   // [nseq, ptiles, 2]: of w, of p
+    double* sums;   // [nseq, tiles, 2]: of w, of p
+    Choice* choice; // [nseq]
     int64_t target_stride, rows, nseq, window;
     int64_t draft_seq_stride, draft_step_stride, probs_seq_stride, probs_step_stride;
     int64_t uniform_stride;
@@ -74,27 +88,34 @@ __device__ __forceinline__ int back_of(const T* row) {
     return static_cast<int>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
 }
 
-// exp(d / temperature) for d <= 0, c = log2(e) / temperature: in fp64, since a drawn number meets
-// the borders of as many tokens as the vocabulary has, and each lies where the sum of all weights
-// before it says (with fp32's exponential one draw in some hundreds lands on the other
-// side of one, with 100,000 tokens). 2^t is 2^n e^x, |x| <= log(2) / 2, and e^x its series
-// to x^10 / 10!, off by 3e-13. Minus infinity and what is below 2^-1000 gives 0.
-__device__ __forceinline__ double exp_of(float d, double c) {
-    const double t = static_cast<double>(d) * c;
-    const double n = __builtin_rint(t);
-    const double x = (t - n) * 0.69314718055994530942;
-    double e = 1. / 3628800.;
-    e = fma(e, x, 1. / 362880.);
-    e = fma(e, x, 1. / 40320.);
-    e = fma(e, x, 1. / 5040.);
-    e = fma(e, x, 1. / 720.);
-    e = fma(e, x, 1. / 120.);
-    e = fma(e, x, 1. / 24.);
-    e = fma(e, x, 1. / 6.);
-    e = fma(e, x, .5);
-    e = fma(e, x, 1.);
-    e = fma(e, x, 1.);
-    return t > -1000. ? __builtin_amdgcn_ldexp(e, static_cast<int>(n)) : 0.;
+// 2^t for t <= 0 or a little above: in fp64, since a drawn number meets the borders of as many tokens
+// as the vocabulary has, and each lies where the sum of all weights before it says (with fp32's
+// exponential one draw in some hundreds lands on the other side of one, with 100,000
+// tokens). 2^t is 2^n 2^x, |x| <= 1/2, and (2^x - 1) / x the polynomial that meets it in the eight
+// Chebyshev points of that range: 2^x is off by 2.2e-12 of itself, and is 1 for 0. n comes from
+// an addition that leaves no bits behind the point. NaN and what is below -1100 gives 0.
+__device__ __forceinline__ double exp2_of(double t) {
+    // (Held in scalar registers: written as they are, each costs a move per product.)
+    double c[8] = {0.6931471805568324,    0.24022650695888503,    0.055504109063258665,
+                   0.00961812913523614,   0.0013333478473685613,  0.0001540347518652791,
+                   1.5303700711328325e-05, 1.3250805518429885e-06};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("" : "+s"(c[i]));
+    constexpr double kWhole = 6755399441055744.;  // 1.5 * 2^52
+    t = fmax(t, -1100.);
+    const double whole = t + kWhole;
+    const double x = t - (whole - kWhole);
+    double e = c[7];
+#pragma unroll
+    for (int i = 6; i >= 0; --i) e = fma(e, x, c[i]);
+    return __builtin_amdgcn_ldexp(fma(e, x, 1.), static_cast<int>(__builtin_bit_cast(int64_t, whole)));
+}
+
+// exp((score - most) / temperature), c = log2(e) / temperature (which may be large: the
+// difference comes first). Scores of infinity weigh 1 among themselves.
+__device__ __forceinline__ double weight_of(float score, float most, double c) {
+    if (most == INFINITY) return score == most ? 1. : 0.;
+    return exp2_of((static_cast<double>(score) - most) * c);
 }
 
 __device__ __forceinline__ double inverse_of(float temperature) {
@@ -110,6 +131,24 @@ __device__ __forceinline__ bool rows_of(const VerifyParams& p, int64_t b, int64_
     return lo >= 0 && hi <= p.rows && lo < hi && hi - lo - 1 <= p.window;
 }
 
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    return v;
+}
+
+// The sum of the lanes up to this one.
+__device__ __forceinline__ double wave_scan(double v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const double below = __shfl_up(v, d);
+        if (lane >= d) v += below;
+    }
+    return v;
+}
+
+// What a and b, sums of weights relative to their largest scores, come to.
 __device__ __forceinline__ Stats merge(Stats a, Stats b, double c) {
     if (b.most > a.most || (b.most == a.most && b.first < a.first)) {
         const Stats t = a;
@@ -117,7 +156,9 @@ __device__ __forceinline__ Stats merge(Stats a, Stats b, double c) {
         b = t;
     }
     // a holds the larger; where the two are equal (infinities too) the factor is 1.
-    if (b.sum > 0.) a.sum += b.sum * (b.most == a.most ? 1. : exp_of(b.most - a.most, c));
+    if (b.sum > 0.)
+        a.sum += b.sum * (b.most == a.most ? 1.
+                                           : exp2_of((static_cast<double>(b.most) - a.most) * c));
     return a;
 }
 
@@ -129,41 +170,50 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(const VerifyParams p) {
     constexpr int E = seg_elements<T>();
     const int tile = blockIdx.x % p.tiles;
     const int64_t r = blockIdx.x / p.tiles;
+    const T* row = static_cast<const T*>(p.target) + r * p.target_stride;
+    const int base = tile * static_cast<int>(tile_elements(sizeof(T))) - back_of(row) +
+                     static_cast<int>(threadIdx.x) * E;
+    float f[kSegs][E];
+#pragma unroll
+    for (int s = 0; s < kSegs; ++s) load_seg<T>(row, base + s * kThreads * E, p.vocab, f[s], -INFINITY);
     const int64_t b = count_starts(p.cu, p.cu64, p.nseq + 1, r) - 1;
     if (b < 0 || b >= p.nseq) return;
     const float temperature = p.temperature[b];
-    const double c = temperature > 0.f ? inverse_of(temperature) : 0.;
-    const T* row = static_cast<const T*>(p.target) + r * p.target_stride;
-    const int base = tile * static_cast<int>(tile_elements(sizeof(T))) - back_of(row);
-    float f[kSegs][E];
-#pragma unroll
-    for (int s = 0; s < kSegs; ++s)
-        load_seg<T>(row, base + (s * kThreads + static_cast<int>(threadIdx.x)) * E, p.vocab, f[s],
-                    -INFINITY);
-    Stats mine = {-INFINITY, INT_MAX, 0.};
+    float most = -INFINITY;  // NaN counts as minus infinity
 #pragma unroll
     for (int s = 0; s < kSegs; ++s)
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-            if (f[s][i] > mine.most) {
-                mine.most = f[s][i];
-                mine.first = base + (s * kThreads + static_cast<int>(threadIdx.x)) * E + i;
-            }
-    if (temperature > 0.f && mine.most > -INFINITY) {
+        for (int i = 0; i < E; ++i) most = fmaxf(most, f[s][i]);
 #pragma unroll
-        for (int s = 0; s < kSegs; ++s)
+    for (int d = 1; d < 64; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
+    Stats mine = {most, INT_MAX, 0.};
+    double c = 0.;
+    if (!(temperature > 0.f)) {
+        if (most > -INFINITY)
 #pragma unroll
-            for (int i = 0; i < E; ++i)
-                // NaN counts as minus infinity.
-                mine.sum += f[s][i] == mine.most  ? 1.
-                            : f[s][i] < mine.most ? exp_of(f[s][i] - mine.most, c)
-                                                  : 0.;
-    }
+            for (int s = kSegs - 1; s >= 0; --s)
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const Stats other = {__shfl_xor(mine.most, d), __shfl_xor(mine.first, d),
-                             __shfl_xor(mine.sum, d)};
-        mine = merge(mine, other, c);
+                for (int i = E - 1; i >= 0; --i)
+                    if (f[s][i] == most) mine.first = base + s * kThreads * E + i;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) mine.first = min(mine.first, __shfl_xor(mine.first, d));
+    } else if (most > -INFINITY) {
+        c = inverse_of(temperature);
+        if (most == INFINITY) {
+#pragma unroll
+            for (int s = 0; s < kSegs; ++s)
+#pragma unroll
+                for (int i = 0; i < E; ++i) mine.sum += f[s][i] == most ? 1. : 0.;
+        } else {
+            double part[4] = {0., 0., 0., 0.};
+#pragma unroll
+            for (int s = 0; s < kSegs; ++s)
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    part[i % 4] += exp2_of((static_cast<double>(f[s][i]) - most) * c);
+            mine.sum = (part[0] + part[1]) + (part[2] + part[3]);
+        }
+        mine.sum = wave_sum(mine.sum);
     }
     __shared__ Stats waves[kWaves];
     if (threadIdx.x % 64 == 0) waves[threadIdx.x / 64] = mine;
@@ -176,36 +226,57 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(const VerifyParams p) {
 
 // --------------------------------------------------------------------- acceptance
 
-// What is known of a row before its weights are read.
-struct Row {
-    float most, temperature;
-    int first;
-    double c, sum;
-};
-
+// Statistics of a row of scores, taken by kLanes neighbouring lanes that share its tiles; each gets
+// the whole.
+constexpr int kLanes = 8;
 __device__ __forceinline__ Row row_stats(const VerifyParams& p, int64_t b, int64_t r) {
     Row row = {0.f, 1.f, 0, 0., 1.};
     if (!p.temperature) return row;
     row.temperature = p.temperature[b];
     if (row.temperature > 0.f) row.c = inverse_of(row.temperature);
-    Stats all = {-INFINITY, INT_MAX, 0.};
-    for (int t = 0; t < p.tiles; ++t) all = merge(all, p.stats[r * p.tiles + t], row.c);
-    row.most = all.most;
-    row.first = all.first == INT_MAX ? 0 : all.first;
-    row.sum = all.sum;
+    const Stats* stats = p.stats + r * p.tiles;
+    const int lane = threadIdx.x % kLanes;
+    float most = -INFINITY;
+    int first = INT_MAX;
+    for (int t = lane; t < p.tiles; t += kLanes) {
+        const Stats s = stats[t];
+        if (s.most > most) {
+            most = s.most;
+            first = s.first;  // of equal ones the first tile's
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < kLanes; d *= 2) {
+        const float other = __shfl_xor(most, d);
+        const int at = __shfl_xor(first, d);
+        if (other > most || (other == most && at < first)) {
+            most = other;
+            first = at;
+        }
+    }
+    double sum = 0.;
+    if (row.temperature > 0.f) {
+        for (int t = lane; t < p.tiles; t += kLanes) {
+            const Stats s = stats[t];
+            if (s.sum > 0.)
+                sum += s.sum *
+                       (s.most == most ? 1. : exp2_of((static_cast<double>(s.most) - most) * row.c));
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < kLanes; d *= 2) sum += __shfl_xor(sum, d);
+    row.most = most;
+    row.first = first == INT_MAX ? 0 : first;
+    row.inverse = 1. / sum;
     return row;
 }
 
 // The probability of a token with this target value, not above 0 as 0.
-__device__ __forceinline__ double chance(const VerifyParams& p, const Row& row, float value, int token,
-                                         double inverse) {
+__device__ __forceinline__ double chance(const VerifyParams& p, const Row& row, float value, int token) {
     if (!p.temperature) return value > 0.f ? static_cast<double>(value) : 0.;
     if (!(row.temperature > 0.f)) return token == row.first ? 1. : 0.;
     if (!(row.most > -INFINITY)) return 0.;
-    return (value == row.most  ? 1.
-            : value < row.most ? exp_of(value - row.most, row.c)
-                               : 0.) *
-           inverse;
+    return weight_of(value, row.most, row.c) * row.inverse;
 }
 
 __device__ __forceinline__ float value_of(const void* base, int dtype, int64_t i) {
@@ -214,49 +285,66 @@ __device__ __forceinline__ float value_of(const void* base, int dtype, int64_t i
     return static_cast<float>(static_cast<const __bf16*>(base)[i]);
 }
 
-// The accepted drafts of a sequence, found by a whole wave: 64 drafts at a time.
+// How many drafts of a sequence are accepted and what is known of the row that follows, found by a
+// whole wave: kLanes lanes a row, as many rows at a time as it has room for.
 template <typename T>
-__device__ __forceinline__ int accepted_of(const VerifyParams& p, int64_t b, int64_t begin, int n) {
+__device__ __forceinline__ Choice choice_of(const VerifyParams& p, int64_t b, int64_t begin, int n) {
     const int lane = threadIdx.x & 63;
-    for (int first = 0; first < n; first += 64) {
-        const int i = first + lane;
+    for (int base = 0;; base += 64 / kLanes) {
+        const int i = base + lane / kLanes;
         bool taken = false;
-        if (i < n) {
-            const int64_t x = load_index(p.drafts, p.draft64,
-                                         b * p.draft_seq_stride + i * p.draft_step_stride);
-            if (x >= 0 && x < p.vocab) {
-                const int64_t r = begin + i;
-                const float value =
-                    static_cast<float>((static_cast<const T*>(p.target) + r * p.target_stride)[x]);
-                const float q = p.probs ? value_of(p.probs, p.probs_dtype,
-                                                   b * p.probs_seq_stride + i * p.probs_step_stride + x)
-                                        : 1.f;
-                const Row row = row_stats(p, b, r);
-                const double px = chance(p, row, value, static_cast<int>(x), 1. / row.sum);
-                taken = static_cast<double>(p.uniforms[b * p.uniform_stride + i]) * q < px;
+        Choice c = {i, i < n, -1, {0.f, 1.f, 0, 0., 1.}};
+        if (i <= n) {
+            const int64_t r = begin + i;
+            const bool draft = i < n;
+            if (draft)
+                c.draft = load_index(p.drafts, p.draft64, b * p.draft_seq_stride + i * p.draft_step_stride);
+            const int64_t x = c.draft;
+            const bool token = x >= 0 && x < p.vocab;
+            float value = 0.f, q = 1.f;
+            double u = 0.;
+            if (token) {
+                value = static_cast<float>((static_cast<const T*>(p.target) + r * p.target_stride)[x]);
+                if (p.probs)
+                    q = value_of(p.probs, p.probs_dtype,
+                                 b * p.probs_seq_stride + i * p.probs_step_stride + x);
+                u = static_cast<double>(p.uniforms[b * p.uniform_stride + i]);
             }
+            c.row = row_stats(p, b, r);
+            taken = token && u * q < chance(p, c.row, value, static_cast<int>(x));
         }
         const unsigned long long missed = ~__ballot(taken);
-        const int stop = missed ? __builtin_ctzll(missed) : 64;
-        if (stop < 64) return first + stop < n ? first + stop : n;
+        if (!missed) continue;  // more rows than these (one past the drafts is never taken)
+        const int from = __builtin_ctzll(missed);
+        Choice o;
+        o.accepted = __shfl(c.accepted, from);
+        o.rejected = __shfl(c.rejected, from);
+        o.draft = __shfl(c.draft, from);
+        o.row.most = __shfl(c.row.most, from);
+        o.row.temperature = __shfl(c.row.temperature, from);
+        o.row.first = __shfl(c.row.first, from);
+        o.row.c = __shfl(c.row.c, from);
+        o.row.inverse = __shfl(c.row.inverse, from);
+        return o;
     }
-    return n;
 }
 
-// The weights of one segment of the row in question: w (what a token is drawn from) and p.
+// A sequence's row that the next token is drawn from.
 template <typename T, typename Q>
-__device__ __forceinline__ void seg_weights(const VerifyParams& p, const Row& row, const T* target,
-                                            const Q* probs, int64_t draft, bool rejected,
-                                            double inverse, int first,
-                                            double (&w)[seg_elements<T>()],
-                                            double (&full)[seg_elements<T>()]) {
-    constexpr int E = seg_elements<T>(), EQ = seg_elements<Q>();
-    float f[E], q[E];
-    load_seg<T>(target, first, p.vocab, f, p.temperature ? -INFINITY : 0.f);
-    if (rejected && probs) {
-        // As many elements of the other row; aligned like this one's or element by element.
-        if (first >= 0 && first + E <= p.vocab && EQ <= E &&
+struct Draw {
+    const T* target;
+    const Q* probs;  // NULL: q is one at the draft, or there is no rejected draft
+    int64_t draft;   // -1: none was rejected
+    Row row;
+
+    // One segment's values of both rows; what lies outside the vocabulary weighs nothing.
+    __device__ __forceinline__ void load(const VerifyParams& p, int first, float (&f)[seg_elements<T>()],
+                                         float (&q)[seg_elements<T>()]) const {
+        constexpr int E = seg_elements<T>(), EQ = seg_elements<Q>();
+        load_seg<T>(target, first, p.vocab, f, p.temperature ? -INFINITY : 0.f);
+        if (probs && first >= 0 && first + E <= p.vocab && EQ <= E &&
             reinterpret_cast<uintptr_t>(probs + first) % 16 == 0) {
+            // As many elements of the other row where it is aligned like this one.
 #pragma unroll
             for (int k = 0; k < E / EQ || k < 1; ++k) {
                 const auto raw = *reinterpret_cast<const typename Words<4>::type*>(probs + first + k * EQ);
@@ -268,76 +356,84 @@ __device__ __forceinline__ void seg_weights(const VerifyParams& p, const Row& ro
         } else {
 #pragma unroll
             for (int i = 0; i < E; ++i)
-                q[i] = first + i >= 0 && first + i < p.vocab ? static_cast<float>(probs[first + i]) : 0.f;
+                q[i] = probs ? (first + i >= 0 && first + i < p.vocab ? static_cast<float>(probs[first + i])
+                                                                      : 0.f)
+                             : (draft >= 0 && first + i == draft ? 1.f : 0.f);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) q[i] = rejected && first + i == draft ? 1.f : 0.f;
     }
+    // Their weights: w (what the token is drawn from) and p. What lies outside the vocabulary has
+    // come as minus infinity (of probabilities: 0).
+    __device__ __forceinline__ void weigh(const VerifyParams& p, const float (&f)[seg_elements<T>()],
+                                          const float (&q)[seg_elements<T>()],
+                                          double (&w)[seg_elements<T>()],
+                                          double (&full)[seg_elements<T>()]) const {
+        constexpr int E = seg_elements<T>();
+        if (!p.temperature) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const bool in = first + i >= 0 && first + i < p.vocab;
-        full[i] = in ? chance(p, row, f[i], first + i, inverse) : 0.;
-        const double left = full[i] - static_cast<double>(q[i]);
-        w[i] = left > 0. ? left : 0.;  // NaN counts as 0
+            for (int i = 0; i < E; ++i) full[i] = f[i] > 0.f ? static_cast<double>(f[i]) : 0.;
+        } else if (!(row.most > -INFINITY)) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) full[i] = 0.;
+        } else if (row.most == INFINITY) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) full[i] = f[i] == INFINITY ? row.inverse : 0.;
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                full[i] = exp2_of((static_cast<double>(f[i]) - row.most) * row.c) * row.inverse;
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const double left = full[i] - static_cast<double>(q[i]);
+            w[i] = left > 0. ? left : 0.;  // NaN counts as 0
+        }
     }
-}
-
-// What both later launches know of a sequence.
-template <typename T, typename Q>
-struct Choice {
-    int64_t begin;
-    int n, accepted;
-    bool rejected;
-    int64_t draft;
-    const T* target;
-    const Q* probs;
-    Row row;
-    double inverse;
-    int back;
 };
 
 template <typename T, typename Q>
-__device__ __forceinline__ bool choose(const VerifyParams& p, int64_t b, Choice<T, Q>* o) {
-    if (!rows_of(p, b, &o->begin, &o->n)) return false;
-    o->accepted = __builtin_amdgcn_readfirstlane(accepted_of<T>(p, b, o->begin, o->n));
-    o->rejected = o->accepted < o->n;
-    const int64_t r = o->begin + o->accepted;
-    o->target = static_cast<const T*>(p.target) + r * p.target_stride;
-    o->probs = o->rejected && p.probs ? static_cast<const Q*>(p.probs) + b * p.probs_seq_stride +
-                                            o->accepted * p.probs_step_stride
-                                      : nullptr;
-    o->draft = o->rejected ? load_index(p.drafts, p.draft64, b * p.draft_seq_stride +
-                                                                 o->accepted * p.draft_step_stride)
-                           : -1;
-    o->row = row_stats(p, b, r);
-    o->inverse = 1. / o->row.sum;
-    o->back = back_of(o->target);
-    return true;
+__device__ __forceinline__ Draw<T, Q> draw_of(const VerifyParams& p, int64_t b, int64_t begin,
+                                              const Choice& c) {
+    Draw<T, Q> o;
+    o.target = static_cast<const T*>(p.target) + (begin + c.accepted) * p.target_stride;
+    o.probs = c.rejected && p.probs ? static_cast<const Q*>(p.probs) + b * p.probs_seq_stride +
+                                          c.accepted * p.probs_step_stride
+                                    : nullptr;
+    o.draft = c.rejected ? c.draft : -1;
+    o.row = c.row;
+    return o;
+}
+
+// A greedy row has one token.
+__device__ __forceinline__ bool greedy(const VerifyParams& p, const Row& row) {
+    return p.temperature && !(row.temperature > 0.f);
 }
 
 // -------------------------------------------------------------------- sums of weights
-
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
-    return v;
-}
 
 template <typename T, typename Q>
 __global__ __launch_bounds__(kThreads) void sums_kernel(const VerifyParams p) {
     constexpr int E = seg_elements<T>();
     const int tile = blockIdx.x % p.tiles;
     const int64_t b = blockIdx.x / p.tiles;
-    Choice<T, Q> o;
-    if (!choose(p, b, &o)) return;
+    int64_t begin;
+    int n;
+    if (!rows_of(p, b, &begin, &n)) return;
+    Choice c = choice_of<T>(p, b, begin, n);
+    c.accepted = __builtin_amdgcn_readfirstlane(c.accepted);
+    c.rejected = __builtin_amdgcn_readfirstlane(c.rejected);
+    if (tile == 0 && threadIdx.x == 0) p.choice[b] = c;
+    if (greedy(p, c.row)) return;
+    const Draw<T, Q> o = draw_of<T, Q>(p, b, begin, c);
+    const int base = tile * static_cast<int>(tile_elements(sizeof(T))) - back_of(o.target) +
+                     static_cast<int>(threadIdx.x) * E;
     double sw = 0., sp = 0.;
+    float f[kSegs][E], q[kSegs][E];
+#pragma unroll
+    for (int s = 0; s < kSegs; ++s) o.load(p, base + s * kThreads * E, f[s], q[s]);
 #pragma unroll
     for (int s = 0; s < kSegs; ++s) {
-        const int first = tile * static_cast<int>(tile_elements(sizeof(T))) - o.back +
-                          (s * kThreads + static_cast<int>(threadIdx.x)) * E;
         double w[E], full[E];
-        seg_weights<T, Q>(p, o.row, o.target, o.probs, o.draft, o.rejected, o.inverse, first, w, full);
+        o.weigh(p, f[s], q[s], w, full);
 #pragma unroll
         for (int i = 0; i < E; ++i) {
             sw += w[i];
@@ -361,113 +457,118 @@ __global__ __launch_bounds__(kThreads) void sums_kernel(const VerifyParams p) {
 
 // ----------------------------------------------------------------------- the token
 
+// The token of a sequence that the drawn number falls to, -1 if none has any weight.
 template <typename T, typename Q>
-__global__ __launch_bounds__(kThreads) void draw_kernel(const VerifyParams p) {
+__device__ __forceinline__ int token_of(const VerifyParams& p, int64_t b, int64_t begin,
+                                        const Choice& c) {
     constexpr int E = seg_elements<T>();
-    const int64_t b = blockIdx.x;
-    int32_t* tokens = p.tokens + b * (p.window + 1);
-    Choice<T, Q> o;
-    if (!choose(p, b, &o)) {
-        for (int64_t i = threadIdx.x; i <= p.window; i += kThreads) tokens[i] = -1;
-        if (threadIdx.x == 0) p.num_accepted[b] = 0;
-        return;
-    }
-    // Every thread adds the tiles' sums in the same order.
+    const Draw<T, Q> o = draw_of<T, Q>(p, b, begin, c);
+    // Every wave takes the tiles' sums, 64 at a time.
     const double* sums = p.sums + b * p.tiles * 2;
-    double total = 0.;
-    for (int t = 0; t < p.tiles; ++t) total += sums[2 * t];
-    const int which = total > 0. ? 0 : 1;
-    if (which) {
-        total = 0.;
-        for (int t = 0; t < p.tiles; ++t) total += sums[2 * t + 1];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    double total[2] = {0., 0.};
+    for (int t = 0; t < p.tiles; t += 64) {
+        const bool in = t + lane < p.tiles;
+        total[0] += wave_sum(in ? sums[2 * (t + lane)] : 0.);
+        total[1] += wave_sum(in ? sums[2 * (t + lane) + 1] : 0.);
     }
-    const double aim = static_cast<double>(p.uniforms[b * p.uniform_stride + p.window]) * total;
+    const int which = total[0] > 0. ? 0 : 1;
+    const double aim = static_cast<double>(p.uniforms[b * p.uniform_stride + p.window]) * total[which];
     // The tile: the first whose running sum passes the aim; where rounding (or a drawn number that
     // is not below 1) leaves none, the last with any weight.
     int tile = -1;
-    double before = 0.;
+    double before = 0., run = 0.;
+    for (int t = 0; t < p.tiles; t += 64) {
+        const double s = t + lane < p.tiles ? sums[2 * (t + lane) + which] : 0.;
+        const double upto = run + wave_scan(s);
+        const unsigned long long any = __ballot(s > 0.), past = __ballot(s > 0. && upto > aim);
+        if (any) {
+            const int at = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(any);
+            tile = t + at;
+            before = __shfl(upto - s, at);
+        }
+        if (past) break;
+        run = __shfl(upto, 63);
+    }
+    if (tile < 0) return -1;
+    // A thread's segments lie side by side here, so that one running sum over the threads orders the
+    // tile.
+    const int base = tile * static_cast<int>(tile_elements(sizeof(T))) - back_of(o.target) +
+                     static_cast<int>(threadIdx.x) * (kSegs * E);
+    double w[kSegs][E], own = 0.;
     {
-        double run = 0.;
-        for (int t = 0; t < p.tiles; ++t) {
-            const double s = sums[2 * t + which];
-            if (!(s > 0.)) continue;
-            tile = t;
-            before = run;
-            run += s;
-            if (run > aim) break;
+        float f[kSegs][E], q[kSegs][E];
+#pragma unroll
+        for (int s = 0; s < kSegs; ++s) o.load(p, base + s * E, f[s], q[s]);
+#pragma unroll
+        for (int s = 0; s < kSegs; ++s) {
+            double full[E];
+            o.weigh(p, f[s], q[s], w[s], full);
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                if (which) w[s][i] = full[i];
+                own += w[s][i];
+            }
         }
     }
     __shared__ double waves[kWaves];
     __shared__ int found[kWaves], last[kWaves];
-    int token = -1;
-    if (tile >= 0) {
-        // A thread's segments lie side by side here, so that one running sum over the threads
-        // orders the tile.
-        double w[kSegs][E], mine = 0.;
+    double sum = wave_scan(own);
+    if (lane == 63) waves[wave] = sum;
+    __syncthreads();
+    sum = before + (sum - own);
+    for (int v = 0; v < wave; ++v) sum += waves[v];
+    int hit = INT_MAX, any = -1;
 #pragma unroll
-        for (int s = 0; s < kSegs; ++s) {
-            const int first = tile * static_cast<int>(tile_elements(sizeof(T))) - o.back +
-                              (static_cast<int>(threadIdx.x) * kSegs + s) * E;
-            double full[E];
-            seg_weights<T, Q>(p, o.row, o.target, o.probs, o.draft, o.rejected, o.inverse, first,
-                              w[s], full);
+    for (int s = 0; s < kSegs; ++s)
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                if (which) w[s][i] = full[i];
-                mine += w[s][i];
-            }
-        }
-        double run = mine;
-        const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const double below = __shfl_up(run, d);
-            if (lane >= d) run += below;
-        }
-        if (lane == 63) waves[wave] = run;
-        __syncthreads();
-        double sum = before + (run - mine);
-        for (int v = 0; v < wave; ++v) sum += waves[v];
-        int hit = INT_MAX, any = -1;
-#pragma unroll
-        for (int s = 0; s < kSegs; ++s) {
-            const int first = tile * static_cast<int>(tile_elements(sizeof(T))) - o.back +
-                              (static_cast<int>(threadIdx.x) * kSegs + s) * E;
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                if (!(w[s][i] > 0.)) continue;
-                sum += w[s][i];
-                any = first + i;
-                if (sum > aim && hit == INT_MAX) hit = first + i;
-            }
+        for (int i = 0; i < E; ++i) {
+            if (!(w[s][i] > 0.)) continue;
+            sum += w[s][i];
+            any = base + s * E + i;
+            if (sum > aim && hit == INT_MAX) hit = any;
         }
 #pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            hit = min(hit, __shfl_xor(hit, d));
-            any = max(any, __shfl_xor(any, d));
-        }
-        if (lane == 0) {
-            found[wave] = hit;
-            last[wave] = any;
-        }
-        __syncthreads();
-        hit = INT_MAX, any = -1;
-        for (int v = 0; v < kWaves; ++v) {
-            hit = min(hit, found[v]);
-            any = max(any, last[v]);
-        }
-        token = hit != INT_MAX ? hit : any;
+    for (int d = 1; d < 64; d *= 2) {
+        hit = min(hit, __shfl_xor(hit, d));
+        any = max(any, __shfl_xor(any, d));
     }
+    if (lane == 0) {
+        found[wave] = hit;
+        last[wave] = any;
+    }
+    __syncthreads();
+    hit = INT_MAX, any = -1;
+    for (int v = 0; v < kWaves; ++v) {
+        hit = min(hit, found[v]);
+        any = max(any, last[v]);
+    }
+    return hit != INT_MAX ? hit : any;
+}
+
+template <typename T, typename Q>
+__global__ __launch_bounds__(kThreads) void draw_kernel(const VerifyParams p) {
+    const int64_t b = blockIdx.x;
+    int32_t* tokens = p.tokens + b * (p.window + 1);
+    int64_t begin;
+    int n;
+    if (!rows_of(p, b, &begin, &n)) {
+        for (int64_t i = threadIdx.x; i <= p.window; i += kThreads) tokens[i] = -1;
+        if (threadIdx.x == 0) p.num_accepted[b] = 0;
+        return;
+    }
+    const Choice c = p.choice[b];
+    const int token = greedy(p, c.row) ? c.row.first : token_of<T, Q>(p, b, begin, c);
     for (int64_t i = threadIdx.x; i <= p.window; i += kThreads) {
         int32_t v = -1;
-        if (i < o.accepted)
+        if (i < c.accepted)
             v = static_cast<int32_t>(load_index(p.drafts, p.draft64,
                                                 b * p.draft_seq_stride + i * p.draft_step_stride));
-        else if (i == o.accepted)
+        else if (i == c.accepted)
             v = token;
         tokens[i] = v;
     }
-    if (threadIdx.x == 0) p.num_accepted[b] = o.accepted + 1;
+    if (threadIdx.x == 0) p.num_accepted[b] = c.accepted + 1;
 }
 
 // ------------------------------------------------------------------------- host
@@ -479,6 +580,7 @@ int64_t round_up(int64_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 int64_t stats_bytes(int64_t rows, int64_t vocab, bool scores) {
     return scores ? round_up(rows * tiles_of(vocab, 4) * static_cast<int64_t>(sizeof(Stats))) : 0;
 }
+int64_t sums_bytes(int64_t nseq, int64_t vocab) { return round_up(nseq * tiles_of(vocab, 4) * 16); }
 
 int check(const ssu_verify_args* a) {
     using ssu::report;
@@ -531,8 +633,8 @@ int check(const ssu_verify_args* a) {
         return report(kBad, "tokens and num_accepted must not be NULL");
     if (!aligned(a->tokens, 4) || !aligned(a->num_accepted, 4))
         return report(kBad, "tokens and num_accepted must be aligned to their dtype");
-    if (!a->workspace || !aligned(a->workspace, kAlign) ||
-        a->workspace_bytes < static_cast<size_t>(ws))
+    if (ws > 0 && (!a->workspace || !aligned(a->workspace, kAlign) ||
+                   a->workspace_bytes < static_cast<size_t>(ws)))
         return report(kBad, "workspace must be 256-byte aligned and hold %lld bytes (got %zu)",
                       (long long)ws, a->workspace_bytes);
     const struct { const char* name; Rows rows; } written[] = {
@@ -581,8 +683,8 @@ extern "C" {
 
 size_t ssu_verify_workspace_bytes(int64_t rows, int64_t nseq, int64_t vocab, int32_t scores) {
     if (rows < 0 || nseq < 0 || vocab < 1) return 0;
-    return static_cast<size_t>(stats_bytes(rows, vocab, scores != 0) +
-                               round_up(nseq * tiles_of(vocab, 4) * 16));
+    return static_cast<size_t>(stats_bytes(rows, vocab, scores != 0) + sums_bytes(nseq, vocab) +
+                               nseq * static_cast<int64_t>(sizeof(Choice)));
 }
 
 int ssu_verify_drafts(const ssu_verify_args* a, void* stream) {
@@ -599,7 +701,9 @@ int ssu_verify_drafts(const ssu_verify_args* a, void* stream) {
     p.num_accepted = a->num_accepted;
     char* ws = static_cast<char*>(a->workspace);
     p.stats = reinterpret_cast<Stats*>(ws);
-    p.sums = reinterpret_cast<double*>(ws + stats_bytes(a->rows, a->vocab, a->temperature != nullptr));
+    ws += stats_bytes(a->rows, a->vocab, a->temperature != nullptr);
+    p.sums = reinterpret_cast<double*>(ws);
+    p.choice = reinterpret_cast<Choice*>(ws + sums_bytes(a->nseq, a->vocab));
     p.target_stride = a->target_stride;
     p.rows = a->rows;
     p.nseq = a->nseq;
