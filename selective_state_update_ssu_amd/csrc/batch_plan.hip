@@ -13,7 +13,7 @@ namespace {
 using namespace layer;
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr int kStretch = 4 * kThreads;  // entries of a table per workgroup
+constexpr int kStretch = kThreads;  // entries of a table per workgroup
 
 struct PlanParams {
     const void* lengths;
@@ -24,6 +24,12 @@ struct PlanParams {
     int64_t nseq, rows, chunk, nchunks, table_stride, table_width, block_size;
     int32_t row_blocks, length64, context64, table64;
 };
+
+// x / y for x >= 0, y > 0: a division of 64 bits takes five times as long as one of 32.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+    if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+    return x / y;
+}
 
 // Running sums of a pair over the workgroup, exclusive, and the totals.
 __device__ __forceinline__ void prefix2(int64_t (&v)[2], int64_t (&total)[2], int64_t (*waves)[2]) {
@@ -74,8 +80,7 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(const PlanParams p) {
         }
         int64_t cut = 0;
         if (p.chunk > 0 && b < p.nseq) {
-            cut = (length + p.chunk - 1) / p.chunk;
-            if (cut < 1) cut = 1;
+            cut = length < 1 ? 1 : 1 + quotient(length - 1, p.chunk);
         }
         int64_t at[2] = {length, cut}, total[2];
         prefix2(at, total, waves);
@@ -118,11 +123,11 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(const PlanParams p) {
                 if (p.row_seq) p.row_seq[i] = static_cast<int32_t>(seq);
                 if (p.row_pos) p.row_pos[i] = static_cast<int32_t>(pos);
                 if (p.row_slots) {
-                    const int64_t column = pos / p.block_size;
+                    const int64_t column = pos < 0 ? p.table_width : quotient(pos, p.block_size);
                     int64_t block = -1;
-                    if (pos >= 0 && column < p.table_width)
+                    if (column < p.table_width)
                         block = load_index(p.table, p.table64, seq * p.table_stride + column);
-                    p.row_slots[i] = block < 0 ? -1 : block * p.block_size + pos % p.block_size;
+                    p.row_slots[i] = block < 0 ? -1 : (block - column) * p.block_size + pos;
                 }
             }
         }
