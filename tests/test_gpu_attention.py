@@ -165,6 +165,13 @@ def test_prompts_cut_into_pieces(delta, lengths, H, G, K, V, io, st):
     prompts(c)
 
 
+def test_delta_prompts_cut_at_their_longer_pieces():
+    """With the delta rule pieces have at least 512 rows."""
+    lengths = [512, 1025, 0, 1540, 1, 513]
+    c = inputs(77, lengths, 1, 1, 64, 24, BF16, F32, True, lead=3, tail=1, inert=(3,))
+    prompts(c)
+
+
 def test_prompts_workspace():
     c = inputs(30, [700, 400], 2, 1, 64, 64, BF16, F32, True)
     cu = torch.tensor(c["cu"], dtype=torch.int32, device=DEV)
