@@ -849,8 +849,10 @@ __device__ __forceinline__ int64_t pieces_of(const Params& p, int64_t b, int* n)
     return uniform64(before);
 }
 
-__device__ __forceinline__ bool inert(const Params& p, int64_t b) {
-    return p.slots && slot_at(p.slots, p.slot64, b, p) < 0;
+// Whether there is a state to hand on. Row ranges that overlap (which is not allowed) can come to
+// more pieces than there is room for: those past it are neither walked nor joined.
+__device__ __forceinline__ bool joined(const Params& p, int64_t b, int64_t first, int n) {
+    return n >= 3 && first + n <= p.pieces && !(p.slots && slot_at(p.slots, p.slot64, b, p) < 0);
 }
 
 static __global__ __launch_bounds__(kChunkThreads) void join_kernel(const Params p) {
@@ -859,7 +861,7 @@ static __global__ __launch_bounds__(kChunkThreads) void join_kernel(const Params
     const int h = static_cast<int>(blockIdx.x / blocks % p.nheads);
     int n;
     const int64_t first = pieces_of(p, b, &n);
-    if (n < 3 || inert(p, b)) return;
+    if (!joined(p, b, first, n)) return;
     const int64_t at = blockIdx.x % blocks * kJoin + 4 * threadIdx.x;
     if (at >= size) return;  // key_dim is a multiple of 8: all four or none
     const int64_t step = p.nheads * size;
@@ -896,7 +898,7 @@ __global__ __launch_bounds__(JoinShape<KP>::THREADS) void join_delta_kernel(cons
     const int h = static_cast<int>(blockIdx.x / blocks % p.nheads);
     int n;
     const int64_t first = pieces_of(p, b, &n);
-    if (n < 3 || inert(p, b)) return;
+    if (!joined(p, b, first, n)) return;
     const int col = static_cast<int>(blockIdx.x % blocks) * COLS + l16;
     const int64_t step = static_cast<int64_t>(p.nheads) * p.V * p.K;
     const int64_t turn = static_cast<int64_t>(p.nheads) * p.K * p.K;

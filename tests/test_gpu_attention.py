@@ -172,6 +172,23 @@ def test_delta_prompts_cut_at_their_longer_pieces():
     prompts(c)
 
 
+@pytest.mark.parametrize("delta", [False, True])
+def test_prompts_overlapping_ranges_stay_in_the_workspace(delta):
+    """Not allowed, with results of no meaning, but nothing outside the workspace is touched: the
+    ranges come to more pieces than there is room for."""
+    rows, K, V = 2048, 64, 64
+    c = inputs(31, [rows], 1, 1, K, V, BF16, F32, delta)
+    cu = torch.tensor([0, rows, 0, rows, 0, rows], dtype=torch.int32, device=DEV)
+    n = ssu.attention_workspace_bytes(rows, 5, 1, K, V, delta)
+    ws = torch.full((n + (1 << 20),), 77, dtype=torch.uint8, device=DEV)
+    state = torch.zeros(5, 1, V, K, device=DEV)
+    q, k, v, decay = (c[x].to(DEV) for x in ("q", "k", "v", "decay"))
+    ssu.linear_attention_varlen(state, q, k, v, decay, cu, workspace=ws,
+                                beta=c["beta"].to(DEV) if delta else None)
+    torch.cuda.synchronize()
+    assert bool((ws[n:] == 77).all())
+
+
 def test_prompts_workspace():
     c = inputs(30, [700, 400], 2, 1, 64, 64, BF16, F32, True)
     cu = torch.tensor(c["cu"], dtype=torch.int32, device=DEV)
