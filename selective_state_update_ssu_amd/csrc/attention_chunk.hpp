@@ -36,6 +36,17 @@
 // (one 16-byte read per operand); k and v with the rows contracted are read transposed. The
 // 16-byte pieces of a row of q or k are permuted by the row (swizzle), so that neither kind of
 // read meets a bank twice.
+//
+// Chunks of 32 rows: with 64 the triangular part doubles per row and P, A and the rows of
+// two chunks (one in use, one on its way in registers) leave fewer waves; it measured no
+// faster, and slower with the delta rule. What bounds it is the issue of instructions: per chunk
+// and wave about 580 vector instructions for 92 matrix ones, a third of them the splitting of S,
+// which every chunk needs anew. 16 prompts of 17,885 rows, 32 heads of 128 x 128 in bf16 with fp32
+// states: 184-204 us (3.3-3.6 TB/s of the 655 MB that have to move; the vector units 38 % busy, matrix
+// cores 24 %, LDS 19 %, and the longest prompt's workgroups outlast the rest: 1.3 waves of 2
+// per SIMD on average), with the delta rule 288-319 us (40 %, 30 %, 18 %). One prompt of 32,768
+// rows, 80 heads of 128 x 64: 550 us (182 ends, 13 join, 480 out under the profiler); one of 4,096
+// rows through the delta rule in fp16: 249 us (142, 28, 109).
 #pragma once
 
 #include <type_traits>
@@ -44,7 +55,6 @@
 #include "attention_common.hpp"
 
 namespace attention {
-
 
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
@@ -170,20 +180,16 @@ struct ChunkShape {
         if (KP == 128) return NC == 2 || NI > 1 || DELTA ? 2 : 3;
         return NI == 1 && wide ? 2 : 1;
     }
-    // LDS row strides; P and A keep what lies on and below the diagonal: rows of a block of 32 have
-    // the columns up to that block's end, A its 16x16 tiles.
-    static constexpr int VS = VW + 8, AS = 20, TILE = 16 * AS;
-    static constexpr int P_SIZE = C == 64 ? 32 * 40 + 32 * 72 : 32 * 40;
+    // LDS row strides; A keeps its 16x16 tiles on and below the diagonal.
+    static constexpr int VS = VW + 8, PS = C + 8, AS = 20, TILE = 16 * AS;
     struct Lds {
         unsigned short k[NI][C][KP], v[NI][C][VS];
-        unsigned short q[OUT ? NI : 1][OUT ? C : 1][OUT ? KP : 8], p[OUT ? NO : 1][OUT ? P_SIZE : 8];
+        unsigned short q[OUT ? NI : 1][OUT ? C : 1][OUT ? KP : 8], p[OUT ? NO : 1][OUT ? C * PS : 8];
         float gh[C], gl[C], eg[C], ew[C], beta[C];
         float a[DELTA ? CT * (CT + 1) / 2 * TILE : 4];
     };
     // Entry of P: row i, place x in the permuted order.
-    static __device__ __forceinline__ int p_at(int i, int x) {
-        return i < 32 ? i * 40 + x : 32 * 40 + (i - 32) * 72 + x;
-    }
+    static __device__ __forceinline__ int p_at(int i, int x) { return i * PS + x; }
     // Place in a row of q or k of (16-byte) piece `piece`. A 16-byte read serves lanes 0-3, 12-15 and
     // 20-27 of 32 at once, that is rows 0-3 and 12-15 of a tile with one piece and rows 4-11 with its
     // neighbour; a transposed one 4 consecutive rows with 4 neighbouring pieces: both find them at
@@ -527,15 +533,15 @@ void chunk_kernel(const Params p) {
             if constexpr (DELTA) a[r] = j < i ? -beta * (a[r] * e) : 0.f;
         }
         if constexpr (OUT) {
-        u32x2 part[NO];
-        split4(s, part);
-        const int to = Shape::p_at(i, 32 * (jt / 2) + 8 * g + 4 * (jt % 2));
+            u32x2 part[NO];
+            split4(s, part);
+            const int to = Shape::p_at(i, 32 * (jt / 2) + 8 * g + 4 * (jt % 2));
 #pragma unroll
-        for (int t = 0; t < NO; ++t) {
-            *reinterpret_cast<u32x2*>(&lds.p[t][to]) = part[t];
-            // The other half of the last 32 columns lies above the diagonal.
-            if (it == jt && it % 2 == 0) *reinterpret_cast<u32x2*>(&lds.p[t][to + 4]) = u32x2{0, 0};
-        }
+            for (int t = 0; t < NO; ++t) {
+                *reinterpret_cast<u32x2*>(&lds.p[t][to]) = part[t];
+                // The other half of the last 32 columns lies above the diagonal.
+                if (it == jt && it % 2 == 0) *reinterpret_cast<u32x2*>(&lds.p[t][to + 4]) = u32x2{0, 0};
+            }
         }
         if constexpr (DELTA)
             *reinterpret_cast<f32x4*>(&lds.a[Shape::a_at(it, jt) + l16 * Shape::AS + 4 * g]) = a;
@@ -692,63 +698,63 @@ void chunk_kernel(const Params p) {
             }
 
             if constexpr (OUT) {
-            u32x4 pf[2][TB][NO];
-            float pe[2];
-            const auto fetch_p = [&](int t) {
-                pe[t % 2] = lds.eg[16 * t + l16];
-#pragma unroll
-                for (int x = 0; x <= t / 2; ++x)
-#pragma unroll
-                    for (int y = 0; y < NO; ++y)
-                        pf[t % 2][x][y] = read16(&lds.p[y][Shape::p_at(16 * t + l16, 32 * x + 8 * g)]);
-            };
-            fetch_p(0);
-            unroll<CT>([&](auto tile) {
-                constexpr int t = decltype(tile)::value;
-                if constexpr (t + 1 < CT) fetch_p(t + 1);
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    O[t][c] *= pe[t % 2];
+                u32x4 pf[2][TB][NO];
+                float pe[2];
+                const auto fetch_p = [&](int t) {
+                    pe[t % 2] = lds.eg[16 * t + l16];
 #pragma unroll
                     for (int x = 0; x <= t / 2; ++x)
-                        O[t][c] = mma_parts<NO - 1>(R[c][x], pf[t % 2][x], O[t][c]);
-                }
-            });
-            if constexpr (WIDE) {
-                const Rsrc ro = range_of(out, n * os);
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const int col = v0 + wv + 16 * c + 4 * g;
-                    const unsigned at = col < p.V ? l16 * os + col * ES : kOutOfRange;
+                        for (int y = 0; y < NO; ++y)
+                            pf[t % 2][x][y] = read16(&lds.p[y][Shape::p_at(16 * t + l16, 32 * x + 8 * g)]);
+                };
+                fetch_p(0);
+                unroll<CT>([&](auto tile) {
+                    constexpr int t = decltype(tile)::value;
+                    if constexpr (t + 1 < CT) fetch_p(t + 1);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        O[t][c] *= pe[t % 2];
+#pragma unroll
+                        for (int x = 0; x <= t / 2; ++x)
+                            O[t][c] = mma_parts<NO - 1>(R[c][x], pf[t % 2][x], O[t][c]);
+                    }
+                });
+                if constexpr (WIDE) {
+                    const Rsrc ro = range_of(out, n * os);
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        const int col = v0 + wv + 16 * c + 4 * g;
+                        const unsigned at = col < p.V ? l16 * os + col * ES : kOutOfRange;
+#pragma unroll
+                        for (int t = 0; t < CT; ++t) {
+                            const f32x4 o = p.scale * O[t][c];
+                            const float y[4] = {o[0], o[1], o[2], o[3]};
+                            const auto w = Raw<IT, 4>::narrow(y);
+                            if constexpr (sizeof(IT) == 4)
+                                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), ro,
+                                                                       at + 16 * t * os, 0, 0);
+                            else
+                                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, w), ro,
+                                                                      at + 16 * t * os, 0, 0);
+                        }
+                    }
+                } else {
 #pragma unroll
                     for (int t = 0; t < CT; ++t) {
-                        const f32x4 o = p.scale * O[t][c];
-                        const float y[4] = {o[0], o[1], o[2], o[3]};
-                        const auto w = Raw<IT, 4>::narrow(y);
-                        if constexpr (sizeof(IT) == 4)
-                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), ro,
-                                                                   at + 16 * t * os, 0, 0);
-                        else
-                            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, w), ro,
-                                                                  at + 16 * t * os, 0, 0);
+                        const int i = 16 * t + l16;
+                        if (i >= n) continue;
+                        IT* o = out + i * p.out_stride;
+#pragma unroll
+                        for (int c = 0; c < NC; ++c)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const int col = v0 + wv + 16 * c + 4 * g + r;
+                                if (col < p.V) o[col] = static_cast<IT>(p.scale * O[t][c][r]);
+                            }
                     }
                 }
-            } else {
-#pragma unroll
-                for (int t = 0; t < CT; ++t) {
-                    const int i = 16 * t + l16;
-                    if (i >= n) continue;
-                    IT* o = out + i * p.out_stride;
-#pragma unroll
-                    for (int c = 0; c < NC; ++c)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int col = v0 + wv + 16 * c + 4 * g + r;
-                            if (col < p.V) o[col] = static_cast<IT>(p.scale * O[t][c][r]);
-                        }
-                }
-            }
             }
 
             // S = e^(G_C) S + k^T (weighted R).

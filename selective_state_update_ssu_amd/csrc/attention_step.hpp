@@ -9,6 +9,8 @@
 //     r = beta (v - e a) or v,   out = scale (e b + r c),   S = e S + r k^T,
 // so that one pass over the registers serves both sums. The state crosses HBM once in
 // each direction, which bounds it; a window's state stays in registers from row to row.
+// 256 sequences, 32 heads of 128 x 128 in fp32, delta rule: 182 us for 1.08 GB, 5.9 TB/s; 64
+// windows of up to 5 rows, a state stored after each: 107 us, 5.0 TB/s; 3 sequences: 5 us.
 #pragma once
 
 #include "attention_common.hpp"

