@@ -258,6 +258,16 @@ PyObject* verify(PyObject* const* arg) {
     return both;
 }
 
+// `n` elements at byte `place` of a tensor of bytes, as a tensor.
+Tensor stretch(const Tensor& whole, int64_t place, int64_t n, at::ScalarType type) {
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
+                                                        c10::scalarTypeToTypeMeta(type));
+    c10::TensorImpl* impl = t.unsafeGetTensorImpl();
+    impl->set_storage_offset(place / static_cast<int64_t>(c10::elementSize(type)));
+    impl->set_sizes_contiguous({n});
+    return t;
+}
+
 // (lengths, rows, chunk_size, nchunks, context_lens, block_table, block_size) -> (cu_seqlens,
 // row_seq, row_pos, cu_chunk_seqlens, seq_idx, last_chunk_indices, row_slots), None for what
 // is not asked for. chunk_size 0: no chunks; nchunks -1: as many as there can be
@@ -300,25 +310,30 @@ PyObject* plan(PyObject* const* arg) {
         a.table_width = table.size(1);
         a.block_table = table.data_ptr();
     }
-    const auto whole = at::TensorOptions().dtype(at::kInt).device(device);
-    std::vector<Tensor> out(7);
-    out[0] = at::empty({a.nseq + 1}, whole);
-    out[1] = at::empty({a.rows}, whole);
-    out[2] = at::empty({a.rows}, whole);
-    a.cu_seqlens = static_cast<int32_t*>(out[0].data_ptr());
-    a.row_seq = static_cast<int32_t*>(out[1].data_ptr());
-    a.row_pos = static_cast<int32_t*>(out[2].data_ptr());
-    if (a.chunk_size > 0) {
-        out[3] = at::empty({a.nchunks + 1}, whole);
-        out[4] = at::empty({a.nchunks}, whole);
-        out[5] = at::empty({a.nseq}, whole);
-        a.cu_chunk_seqlens = static_cast<int32_t*>(out[3].data_ptr());
-        a.seq_idx = static_cast<int32_t*>(out[4].data_ptr());
-        a.last_chunk_indices = static_cast<int32_t*>(out[5].data_ptr());
-    }
-    if (table.defined()) {
-        out[6] = at::empty({a.rows}, whole.dtype(at::kLong));
-        a.row_slots = static_cast<int64_t*>(out[6].data_ptr());
+    // One allocation for all tables: each of its own costs as much as the launch.
+    const bool chunks = a.chunk_size > 0;
+    const int64_t sizes[7] = {a.nseq + 1, a.rows, a.rows, chunks ? a.nchunks + 1 : -1,
+                              chunks ? a.nchunks : -1, chunks ? a.nseq : -1,
+                              table.defined() ? a.rows : -1};
+    const auto bytes = [&](int i) {
+        return sizes[i] < 0 ? 0 : (sizes[i] * (i == 6 ? 8 : 4) + 63) / 64 * 64;
+    };
+    int64_t total = 0;
+    for (int i = 0; i < 7; ++i) total += bytes(i);
+    const Tensor whole = at::empty({total}, at::TensorOptions().dtype(at::kByte).device(device));
+    void** const at[7] = {reinterpret_cast<void**>(&a.cu_seqlens), reinterpret_cast<void**>(&a.row_seq),
+                          reinterpret_cast<void**>(&a.row_pos),
+                          reinterpret_cast<void**>(&a.cu_chunk_seqlens),
+                          reinterpret_cast<void**>(&a.seq_idx),
+                          reinterpret_cast<void**>(&a.last_chunk_indices),
+                          reinterpret_cast<void**>(&a.row_slots)};
+    Tensor out[7];
+    int64_t place = 0;
+    for (int i = 0; i < 7; ++i) {
+        if (sizes[i] < 0) continue;
+        out[i] = stretch(whole, place, sizes[i], i == 6 ? at::kLong : at::kInt);
+        *at[i] = static_cast<char*>(whole.data_ptr()) + place;
+        place += bytes(i);
     }
     call("ssu_batch_plan", ssu_batch_plan, a, device);
     PyObject* tuple = PyTuple_New(7);
