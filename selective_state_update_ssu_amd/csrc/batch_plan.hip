@@ -1,12 +1,12 @@
 // batch_plan.hip -- tables of a packed batch from its lengths (semantics in include/batch.h).
 //
-// One launch. Every workgroup sums the lengths (1,024 at a time, a running sum of rows and of
+// One launch. Every workgroup sums the lengths (2,048 at a time, a running sum of rows and of
 // chunks) and fills one stretch of a table: of the rows, or of the chunks; each entry is
 // found by bisection among the sums in LDS. The first workgroup writes what there is one of per
 // request. Summing again in every workgroup costs less than a second launch, which would
-// have to wait for the sums: the call is latency. 5 requests: 9.4 us, of which the kernel 5; 2,000
-// with 130,001 rows, chunks and slots: 10.6 us (14.6 with four entries per thread and 64-bit
-// divisions).
+// have to wait for the sums: the call is latency. 5 requests: 5.9 us; 2,000 with 130,001
+// rows, chunks and slots: 7.7 us (10.7 with one request per thread, 8.3 with four, which costs the
+// few requests 0.4; 14.6 with four entries of a table per thread and 64-bit divisions).
 #include "batch.h"
 #include "layer_common.hpp"
 
@@ -16,6 +16,7 @@ using namespace layer;
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kStretch = kThreads;  // entries of a table per workgroup
+constexpr int kEach = 2, kHeld = kEach * kThreads;  // requests of a thread, of a pass
 
 struct PlanParams {
     const void* lengths;
@@ -66,45 +67,53 @@ __device__ __forceinline__ void prefix2(int64_t (&v)[2], int64_t (&total)[2], in
 
 __global__ __launch_bounds__(kThreads) void plan_kernel(const PlanParams p) {
     __shared__ int64_t waves[kWaves][2];
-    __shared__ int64_t starts[2][kThreads + 1];  // of the requests at hand: first row, first chunk
+    __shared__ int64_t starts[2][kHeld + 1];  // of the requests at hand: first row, first chunk
     const bool chunks = static_cast<int>(blockIdx.x) >= p.row_blocks;
     const int64_t stretch = chunks ? blockIdx.x - p.row_blocks : blockIdx.x;
     const int64_t lo = stretch * kStretch;
     const int64_t most = chunks ? p.nchunks + 1 : p.rows;
     const int64_t hi = lo + kStretch < most ? lo + kStretch : most;
     int64_t base[2] = {0, 0};
-    for (int64_t b0 = 0; b0 < p.nseq; b0 += kThreads) {
-        const int64_t b = b0 + threadIdx.x;
-        int64_t length = 0;
-        if (b < p.nseq) {
-            length = load_index(p.lengths, p.length64, b);
-            if (length < 0) length = 0;
+    for (int64_t b0 = 0; b0 < p.nseq; b0 += kHeld) {
+        const int own = threadIdx.x * kEach;
+        int64_t length[kEach] = {}, cut[kEach] = {}, at[2] = {0, 0}, total[2];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            if (b0 + own + k >= p.nseq) continue;
+            length[k] = load_index(p.lengths, p.length64, b0 + own + k);
+            if (length[k] < 0) length[k] = 0;
+            if (p.chunk > 0) cut[k] = length[k] < 1 ? 1 : 1 + quotient(length[k] - 1, p.chunk);
+            at[0] += length[k];
+            at[1] += cut[k];
         }
-        int64_t cut = 0;
-        if (p.chunk > 0 && b < p.nseq) {
-            cut = length < 1 ? 1 : 1 + quotient(length - 1, p.chunk);
-        }
-        int64_t at[2] = {length, cut}, total[2];
         prefix2(at, total, waves);
-        starts[0][threadIdx.x] = base[0] + at[0];
-        starts[1][threadIdx.x] = base[1] + at[1];
-        if (threadIdx.x == 0) {
-            starts[0][kThreads] = base[0] + total[0];
-            starts[1][kThreads] = base[1] + total[1];
-        }
-        if (blockIdx.x == 0 && b < p.nseq) {
-            if (p.cu) p.cu[b] = static_cast<int32_t>(base[0] + at[0]);
-            if (p.last) {
-                const int64_t c = base[1] + at[1] + cut - 1;
-                p.last[b] = c < p.nchunks ? static_cast<int32_t>(c) : -1;
+        at[0] += base[0];
+        at[1] += base[1];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int64_t b = b0 + own + k;
+            starts[0][own + k] = at[0];
+            starts[1][own + k] = at[1];
+            if (blockIdx.x == 0 && b < p.nseq) {
+                if (p.cu) p.cu[b] = static_cast<int32_t>(at[0]);
+                if (p.last) {
+                    const int64_t c = at[1] + cut[k] - 1;
+                    p.last[b] = c < p.nchunks ? static_cast<int32_t>(c) : -1;
+                }
             }
+            at[0] += length[k];
+            at[1] += cut[k];
+        }
+        if (threadIdx.x == 0) {
+            starts[0][kHeld] = base[0] + total[0];
+            starts[1][kHeld] = base[1] + total[1];
         }
         __syncthreads();
         // Entries of these requests in the stretch.
         const int64_t* s = starts[chunks ? 1 : 0];
         const int64_t from = s[0] > lo ? s[0] : lo;
-        const int64_t end = s[kThreads] < hi ? s[kThreads] : hi;
-        const int held = static_cast<int>(p.nseq - b0 < kThreads ? p.nseq - b0 : kThreads);
+        const int64_t end = s[kHeld] < hi ? s[kHeld] : hi;
+        const int held = static_cast<int>(p.nseq - b0 < kHeld ? p.nseq - b0 : kHeld);
         for (int64_t i = from + threadIdx.x; i < end; i += kThreads) {
             int x = 0, y = held;  // s[x] <= i < s[y]
             while (y - x > 1) {

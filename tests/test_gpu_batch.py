@@ -234,6 +234,27 @@ def test_plan(idx, chunk, lengths):
     plan(lengths, rows, chunk, context=context, table=table, block=16, idx=idx)
 
 
+@pytest.mark.parametrize("n", [4095, 4096, 4097, 9000])
+def test_plan_of_many_requests(n):
+    g = torch.Generator().manual_seed(n)
+    lengths = torch.randint(-1, 6, (n,), generator=g).tolist()
+    plan(lengths, sum(max(x, 0) for x in lengths) + 5, 2)
+    plan(lengths, n, 4)
+
+
+def test_plan_tables_are_tensors_of_their_own():
+    """Tables share an allocation, and nothing else: writing one leaves the others."""
+    got = ssu.batch_plan(torch.tensor([3, 0, 4], device=DEV), 9, chunk_size=2,
+                         block_table=torch.zeros(3, 9, dtype=torch.int32, device=DEV))
+    before = [t.clone() for t in got]
+    for i, t in enumerate(got):
+        assert t.is_contiguous() and not t.requires_grad
+        t.fill_(-7)
+        for j, other in enumerate(got):
+            assert torch.equal(other, before[j]) == (i != j)
+        t.copy_(before[i])
+
+
 def test_plan_lengths_that_pass_the_rows():
     plan([10, 20, 30], 25, 8)
     plan([10, 20, 30], 25, 8, nchunks=3)
