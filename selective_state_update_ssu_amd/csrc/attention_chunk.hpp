@@ -177,7 +177,7 @@ struct ChunkShape {
     // Workgroups of a compute unit (waves of a SIMD), as many as registers allow without spilling.
     static constexpr int waves(bool wide) {
         if (KP == 64) return NC == 2 ? 2 : NI == 3 || !wide ? 2 : DELTA ? 3 : 4;
-        if (KP == 128) return NC == 2 || NI > 1 || DELTA ? 2 : 3;
+        if (KP == 128) return NC == 2 || NI > 1 || DELTA ? 2 : wide ? 4 : 3;
         return NI == 1 && wide ? 2 : 1;
     }
     // LDS row strides; A keeps its 16x16 tiles on and below the diagonal.
@@ -537,15 +537,18 @@ void chunk_kernel(const Params p) {
             split4(s, part);
             const int to = Shape::p_at(i, 32 * (jt / 2) + 8 * g + 4 * (jt % 2));
 #pragma unroll
-            for (int t = 0; t < NO; ++t) {
-                *reinterpret_cast<u32x2*>(&lds.p[t][to]) = part[t];
-                // The other half of the last 32 columns lies above the diagonal.
-                if (it == jt && it % 2 == 0) *reinterpret_cast<u32x2*>(&lds.p[t][to + 4]) = u32x2{0, 0};
-            }
+            for (int t = 0; t < NO; ++t) *reinterpret_cast<u32x2*>(&lds.p[t][to]) = part[t];
         }
         if constexpr (DELTA)
             *reinterpret_cast<f32x4*>(&lds.a[Shape::a_at(it, jt) + l16 * Shape::AS + 4 * g]) = a;
     };
+
+    // The half of the first 16 rows of P that lies above the diagonal.
+    if constexpr (OUT)
+        if (wave == 0)
+#pragma unroll
+            for (int t = 0; t < NO; ++t)
+                *reinterpret_cast<u32x2*>(&lds.p[t][Shape::p_at(l16, 8 * g + 4)]) = u32x2{0, 0};
 
     float total = 0.f;  // decay of the piece, as an exponent of 2
     load(0);
@@ -815,12 +818,14 @@ void chunk_kernel(const Params p) {
 
     // ---- the state after the last row
     if (OUT && !piece.last) return;
+    int at_lane = lane;
+    asm volatile("" : "+v"(at_lane));  // or the places of the entering state stay in registers until here
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        const int col = v0 + wv + 16 * c + l16;
+        const int col = v0 + wv + 16 * c + at_lane % 16;
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
-            const int key = 16 * t + 4 * g;
+            const int key = 16 * t + 4 * (at_lane / 16);
             if (col >= columns || key >= p.K) continue;
             const int64_t at = static_cast<int64_t>(col) * p.K + key;
             if constexpr (OUT)
