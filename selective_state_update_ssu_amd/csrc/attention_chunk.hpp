@@ -42,11 +42,11 @@
 // faster, and slower with the delta rule. What bounds it is the issue of instructions: per chunk
 // and wave about 580 vector instructions for 92 matrix ones, a third of them the splitting of S,
 // which every chunk needs anew. 16 prompts of 17,885 rows, 32 heads of 128 x 128 in bf16 with fp32
-// states: 184-204 us (3.3-3.6 TB/s of the 655 MB that have to move; the vector units 38 % busy, matrix
+// states: 180-200 us (3.3-3.6 TB/s of the 655 MB that have to move; the vector units 38 % busy, matrix
 // cores 24 %, LDS 19 %, and the longest prompt's workgroups outlast the rest: 1.3 waves of 2
-// per SIMD on average), with the delta rule 288-319 us (40 %, 30 %, 18 %). One prompt of 32,768
-// rows, 80 heads of 128 x 64: 550 us (182 ends, 13 join, 480 out under the profiler); one of 4,096
-// rows through the delta rule in fp16: 249 us (142, 28, 109).
+// per SIMD on average), with the delta rule 286-319 us (40 %, 30 %, 18 %). One prompt of 32,768
+// rows, 80 heads of 128 x 64: 531-580 us (a quarter of it the ends of pieces); one of 4,096 rows
+// through the delta rule in fp16: 245 us (half of it the ends).
 #pragma once
 
 #include <type_traits>
@@ -1029,7 +1029,7 @@ hipError_t launch_passes(const Params& p, hipStream_t stream) {
         if (e != hipSuccess) return e;
     }
     // Slices of 128 columns read q, k and P half as often: 2.8 us against 3.1 for 64 rows x 64
-    // columns on a full card (delta rule 4.2 against 4.9). Where workgroups are few, or registers
+    // columns on a full card (delta rule 4.2 against 4.9), though these have four waves per SIMD. Where workgroups are few, or registers
     // are (inputs of several parts, keys of more than 128), slices of 64.
     if constexpr (std::is_same<IT, __bf16>::value && KP <= 128 && WIDE)
         if (p.piece == 0 && p.V > 64) return launch_out<IT, KP, 2, DELTA, WIDE>(p, stream);
