@@ -17,9 +17,9 @@
 // Where the sequences alone give too few workgroups they are cut into pieces. A first launch
 // walks all but each sequence's last piece for the state alone (kEnds), a second hands
 // the states on from piece to piece, and the last starts every piece from the state that enters it
-// (kOut). A piece changes its entering state to M S + N: N is what it makes of zeros. Without the
-// delta rule M is its decay; with it M is what it makes of the identity as a state with no
-// values, walked as further value columns.
+// (kOut); the slot's own, which the last launch overwrites, is kept by the first. A piece changes its
+// entering state to M S + N: N is what it makes of zeros. Without the delta rule M is its decay; with
+// it M is what it makes of the identity as a state with no values, walked as further value columns.
 //
 // Precision: the matrix cores take bf16, so a number goes in as parts of 8 bits: bf16 inputs as
 // one (exactly), fp16 as two (exactly), fp32 as three; what is derived and reaches the state (S,
@@ -72,6 +72,40 @@ __device__ __forceinline__ Rsrc range_of(const void* base, unsigned bytes) {
                                              0x00020000);
 }
 constexpr unsigned kOutOfRange = 0x80000000u;
+
+// Four consecutive elements of a state at element i of a range, as load4 and store4; i of kOutOfRange / 4
+// or more lies past any.
+template <typename ST>
+__device__ __forceinline__ f32x4 load4(Rsrc r, unsigned i) {
+    float f[4];
+    if constexpr (sizeof(ST) == 4)
+        Raw<ST, 4>::widen(__builtin_bit_cast(typename Raw<ST, 4>::type,
+                                             __builtin_amdgcn_raw_buffer_load_b128(r, 4 * i, 0, 0)), f);
+    else
+        Raw<ST, 4>::widen(__builtin_bit_cast(typename Raw<ST, 4>::type,
+                                             __builtin_amdgcn_raw_buffer_load_b64(r, 2 * i, 0, 0)), f);
+    return f32x4{f[0], f[1], f[2], f[3]};
+}
+template <typename ST>
+__device__ __forceinline__ void store4(Rsrc r, unsigned i, f32x4 v) {
+    const float f[4] = {v[0], v[1], v[2], v[3]};
+    const auto w = Raw<ST, 4>::narrow(f);
+    if constexpr (sizeof(ST) == 4)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), r, 4 * i, 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, w), r, 2 * i, 0, 0);
+}
+
+// f(T()) with the element type of a state.
+template <typename F>
+__device__ __forceinline__ void of_dtype(int dtype, F&& f) {
+    if (dtype == SSU_F32)
+        f(float());
+    else if (dtype == SSU_F16)
+        f(_Float16());
+    else
+        f(__bf16());
+}
 
 __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
@@ -258,6 +292,7 @@ __device__ __forceinline__ void wave_fence() {
 // The piece of a sequence that a workgroup walks.
 struct Piece {
     int64_t b, begin, rows;  // sequence, first row in the call, rows
+    int64_t behind;          // pieces of the sequence behind this one
     bool first, last;        // of the sequence
 };
 
@@ -286,6 +321,7 @@ __device__ __forceinline__ bool locate(const Params& p, int64_t pi, Piece* o) {
         o->b = b;
         o->rows = uniform64(rows_of(p, b, &begin));
         o->begin = uniform64(begin);
+        o->behind = 0;
         o->first = o->last = true;
         return o->rows > 0;
     }
@@ -308,6 +344,7 @@ __device__ __forceinline__ bool locate(const Params& p, int64_t pi, Piece* o) {
                                              __builtin_amdgcn_readlane(mine, at));
             o->b = b0 + at;
             o->begin = layer::lane64(begin, at) + j * p.piece;
+            o->behind = __builtin_amdgcn_readlane(mine, at) - 1 - j;
             o->first = j == 0;
             o->last = (j + 1) * p.piece >= rows;
             o->rows = o->last ? rows - j * p.piece : p.piece;
@@ -348,7 +385,20 @@ void chunk_kernel(const Params p) {
     if (slot < 0) return;
     // Columns of the identity lie behind those of the values.
     const bool values = OUT || !DELTA || slice < p.value_blocks;
-    if (!OUT && (piece.last || (!values && piece.first))) return;
+    const int64_t in_slot = slot * p.slot_stride + static_cast<int64_t>(h) * p.V * p.K;
+    // A piece's own place for states: [pieces, heads, value, key], transitions behind them.
+    const int64_t in_ends = (pi * p.nheads + h) * p.V * p.K;
+    if constexpr (!OUT) {
+        // A last piece's end goes to the slot, in the launch in which the sequence's first piece needs
+        // the state that was there: its place keeps that one.
+        if (piece.last && !piece.first && values && p.has && p.has[piece.b]) {
+            const int from = slice * VW * p.K;
+            const int to = (slice + 1) * VW < p.V ? from + VW * p.K : p.V * p.K;
+            for (int i = from + 4 * tid; i < to; i += 4 * kChunkThreads)
+                store4<float>(p.ends, in_ends + i, state_load4(p.state, p.state_dtype, in_slot + i));
+        }
+        if (piece.last || (!values && piece.first)) return;
+    }
     const int64_t begin = piece.begin, n_all = piece.rows;
     const int columns = values ? p.V : p.K;
     const int kg = h / p.per_group;
@@ -360,31 +410,45 @@ void chunk_kernel(const Params p) {
     const IT* v = static_cast<const IT*>(p.v) + begin * p.v_stride + static_cast<int64_t>(h) * p.V;
     IT* out = static_cast<IT*>(p.out) + begin * p.out_stride + static_cast<int64_t>(h) * p.V;
     const float* decay = p.decay + begin * p.decay_stride + h;
+    const void* beta = nullptr;
+    if constexpr (DELTA)
+        beta = static_cast<const char*>(p.beta) +
+               (begin * p.beta_stride + h) * (p.beta_f32 ? 4 : static_cast<int>(ES));
 
     // ---- the entering state
     f32x4 S[NC][KT];
-    const bool has = values && (!piece.first || (p.has && p.has[piece.b]));
-    const int64_t in_slot = slot * p.slot_stride + static_cast<int64_t>(h) * p.V * p.K;
-    // A piece's own place for states: [pieces, heads, value, key], transitions behind them.
-    const int64_t in_ends = (pi * p.nheads + h) * p.V * p.K;
-    const int64_t enter = in_ends - static_cast<int64_t>(p.nheads) * p.V * p.K;  // of the piece before
+    const bool has = values && (piece.first ? p.has && p.has[piece.b] : OUT);
+    // The slot is read where no other workgroup of the launch writes it: by the first launch and by
+    // sequences of one piece (and, of ranges that overlap, where the last piece is past the workspace and
+    // not walked). Else the state lies in `ends`: of a first piece in the last one's place, of
+    // another in that of the piece before it.
+    const bool of_slot = piece.first && (!OUT || piece.last || pi + piece.behind >= p.pieces);
+    const int dtype = of_slot ? p.state_dtype : SSU_F32;
+    const int in_size = dtype == SSU_F32 ? 4 : 2;
+    const void* enter = static_cast<const char*>(p.state) + in_slot * in_size;
+    if (!of_slot)
+        enter = p.ends + in_ends +
+                (piece.first ? piece.behind : -1) * static_cast<int64_t>(p.nheads) * p.V * p.K;
+    // A lane's four keys of column tile c and key tile t, in a range that ends with the last column.
+    const auto place = [&](int of_lane, int c, int t) {
+        const unsigned col = v0 + wv + 16 * c + of_lane % 16, key = 16 * t + 4 * (of_lane / 16);
+        return key < static_cast<unsigned>(p.K) ? col * p.K + key : kOutOfRange / 4;
+    };
+    of_dtype(dtype, [&](auto type) {
+        const Rsrc from = range_of(enter, has ? p.V * p.K * in_size : 0);
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        const int col = v0 + wv + 16 * c + l16;
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
-            S[c][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-            const int key = 16 * t + 4 * g;
-            const int64_t at = static_cast<int64_t>(col) * p.K + key;
-            if (!OUT && !values)
+            for (int t = 0; t < KT; ++t) S[c][t] = load4<decltype(type)>(from, place(lane, c, t));
+    });
+    if (!OUT && !values)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) S[c][t][i] = key + i == col ? 1.f : 0.f;
-            if (has && col < p.V && key < p.K)
-                S[c][t] = piece.first ? state_load4(p.state, p.state_dtype, in_slot + at)
-                          : OUT       ? load4<float>(p.ends, enter + at)
-                                      : f32x4{0.f, 0.f, 0.f, 0.f};
-        }
-    }
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    S[c][t][i] = 16 * t + 4 * g + i == v0 + wv + 16 * c + l16 ? 1.f : 0.f;
 
     // ---- what a thread moves of a chunk: its segments of q, k and v, one row's decay and beta.
     // Segment i lies QROWS (VROWS) rows behind segment i - 1, in the same columns.
@@ -435,11 +499,11 @@ void chunk_kernel(const Params p) {
         const int64_t row = first + lane < n_all ? first + lane : n_all - 1;
         gr = decay[row * p.decay_stride];
         if constexpr (DELTA) {
-            const int64_t at = (begin + row) * p.beta_stride + h;
+            const int64_t at = row * p.beta_stride;
             if (p.beta_f32)
-                br = static_cast<const unsigned*>(p.beta)[at];
+                br = static_cast<const unsigned*>(beta)[at];
             else
-                br = static_cast<const typename Bits<IT>::type*>(p.beta)[at];
+                br = static_cast<const typename Bits<IT>::type*>(beta)[at];
         }
     };
     const auto store = [&](int n) {
@@ -506,7 +570,7 @@ void chunk_kernel(const Params p) {
 
     // ---- tile (it, jt) of the scores, and of A
     const auto scores = [&](int it, int jt) {
-        const int i = 16 * it + l16;
+        const int i = 16 * it + l16, ahead = i - (16 * jt + 4 * g);  // of the lane's first column
         f32x4 s = {0.f, 0.f, 0.f, 0.f}, a = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int x = 0; x < KB; ++x) {
@@ -527,10 +591,9 @@ void chunk_kernel(const Params p) {
         if constexpr (DELTA) beta = lds.beta[i];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int j = 16 * jt + 4 * g + r;
             const float e = __builtin_amdgcn_exp2f((gh - jh[r]) + (gl - jl[r]));
-            s[r] = j <= i ? s[r] * e : 0.f;
-            if constexpr (DELTA) a[r] = j < i ? -beta * (a[r] * e) : 0.f;
+            s[r] = ahead > r - 1 ? s[r] * e : 0.f;
+            if constexpr (DELTA) a[r] = ahead > r ? -beta * (a[r] * e) : 0.f;
         }
         if constexpr (OUT) {
             u32x2 part[NO];
@@ -732,8 +795,9 @@ void chunk_kernel(const Params p) {
                         const unsigned at = col < p.V ? l16 * os + col * ES : kOutOfRange;
 #pragma unroll
                         for (int t = 0; t < CT; ++t) {
-                            const f32x4 o = p.scale * O[t][c];
-                            const float y[4] = {o[0], o[1], o[2], o[3]};
+                            float y[4];
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) y[r] = p.scale * O[t][c][r];
                             const auto w = Raw<IT, 4>::narrow(y);
                             if constexpr (sizeof(IT) == 4)
                                 __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), ro,
@@ -820,22 +884,20 @@ void chunk_kernel(const Params p) {
     if (OUT && !piece.last) return;
     int at_lane = lane;
     asm volatile("" : "+v"(at_lane));  // or the places of the entering state stay in registers until here
+    const auto leave = [&](void* to, auto type) {
+        typedef decltype(type) ST;
+        const Rsrc r = range_of(to, columns * p.K * static_cast<int>(sizeof(ST)));
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        const int col = v0 + wv + 16 * c + at_lane % 16;
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
-            const int key = 16 * t + 4 * (at_lane / 16);
-            if (col >= columns || key >= p.K) continue;
-            const int64_t at = static_cast<int64_t>(col) * p.K + key;
-            if constexpr (OUT)
-                state_store4(p.state, p.state_dtype, in_slot + at, S[c][t]);
-            else if (values)
-                store4<float>(p.ends, in_ends + at, S[c][t]);
-            else
-                store4<float>(p.moves, (pi * p.nheads + h) * p.K * p.K + at, S[c][t]);
-        }
-    }
+            for (int t = 0; t < KT; ++t) store4<ST>(r, place(at_lane, c, t), S[c][t]);
+    };
+    if constexpr (OUT)
+        of_dtype(p.state_dtype, [&](auto type) {
+            leave(static_cast<decltype(type)*>(p.state) + in_slot, type);
+        });
+    else
+        leave(values ? p.ends + in_ends : p.moves + (pi * p.nheads + h) * p.K * p.K, float());
     if constexpr (!OUT && !DELTA)
         if (tid == 0 && slice == 0) p.sums[pi * p.nheads + h] = __builtin_amdgcn_exp2f(total);
 }

@@ -79,15 +79,6 @@ __device__ __forceinline__ f32x4 state_load4(const void* p, int dtype, int64_t i
     return dtype == SSU_F32 ? load4<float>(p, i)
            : dtype == SSU_F16 ? load4<_Float16>(p, i) : load4<__bf16>(p, i);
 }
-__device__ __forceinline__ void state_store4(void* p, int dtype, int64_t i, f32x4 v) {
-    if (dtype == SSU_F32)
-        store4<float>(p, i, v);
-    else if (dtype == SSU_F16)
-        store4<_Float16>(p, i, v);
-    else
-        store4<__bf16>(p, i, v);
-}
-
 // Launchers of one io type's kernels, each in a translation unit of its own.
 hipError_t step_f32(const Params& p, bool packed, hipStream_t stream);
 hipError_t step_f16(const Params& p, bool packed, hipStream_t stream);
