@@ -381,7 +381,7 @@ void chunk_kernel(const Params p) {
     const int h = static_cast<int>(item % per_piece) / p.blocks, slice = static_cast<int>(item % per_piece) % p.blocks;
     Piece piece;
     if (!locate(p, pi, &piece)) return;
-    const int64_t slot = uniform64(p.slots ? slot_at(p.slots, p.slot64, piece.b, p) : piece.b);
+    const int64_t slot = uniform64(slot_of(p, piece.b));
     if (slot < 0) return;
     // Columns of the identity lie behind those of the values.
     const bool values = OUT || !DELTA || slice < p.value_blocks;
@@ -925,7 +925,7 @@ __device__ __forceinline__ int64_t pieces_of(const Params& p, int64_t b, int* n)
 // Whether there is a state to hand on. Row ranges that overlap (which is not allowed) can come to
 // more pieces than there is room for: those past it are neither walked nor joined.
 __device__ __forceinline__ bool joined(const Params& p, int64_t b, int64_t first, int n) {
-    return n >= 3 && first + n <= p.pieces && !(p.slots && slot_at(p.slots, p.slot64, b, p) < 0);
+    return n >= 3 && first + n <= p.pieces && slot_of(p, b) >= 0;
 }
 
 static __global__ __launch_bounds__(kChunkThreads) void join_kernel(const Params p) {

@@ -54,11 +54,18 @@ constexpr float kLog2e = layer::kLog2e;
 // fp32, and differences of running sums stay free of infinity minus infinity.
 __device__ __forceinline__ float decay_of(float g) { return fmaxf(g, -300.f); }
 
-// The slot named by entry `at` of a table, -1 if it is inert.
+// A slot's id, -1 if it is inert.
+__device__ __forceinline__ int64_t usable(int64_t s, const Params& p) {
+    return s == p.pad_slot_id || s < 0 || s >= p.nslots ? -1 : s;
+}
+// The slot named by entry `at` of a table.
 __device__ __forceinline__ int64_t slot_at(const void* table, int is64, int64_t at,
                                            const Params& p) {
-    const int64_t s = load_index(table, is64, at);
-    return s == p.pad_slot_id || s < 0 || s >= p.nslots ? -1 : s;
+    return usable(load_index(table, is64, at), p);
+}
+// The slot of sequence b where it has one.
+__device__ __forceinline__ int64_t slot_of(const Params& p, int64_t b) {
+    return p.slots ? slot_at(p.slots, p.slot64, b, p) : usable(b, p);
 }
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));

@@ -78,9 +78,9 @@ __global__ __launch_bounds__(kStepThreads) void step_kernel(const Params p) {
         if (p.na && (kept < 1 || kept > p.steps)) return;
         from = p.slots ? slot_at(p.slots, p.slot64,
                                  b * p.slot_seq_stride + (kept - 1) * p.slot_step_stride, p)
-                       : b;
+                       : usable(b, p);
     } else {
-        from = p.slots ? slot_at(p.slots, p.slot64, b, p) : b;
+        from = slot_of(p, b);
     }
     from = uniform64(from);
     if (from < 0) return;
