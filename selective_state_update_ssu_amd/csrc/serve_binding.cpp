@@ -42,6 +42,9 @@ int64_t table_of(const char* name, const Tensor& t, int64_t nseq, at::Device dev
         if (t.size(0) != nseq)
             value_error(std::string(name) + " must have one row per sequence (" +
                         std::to_string(nseq) + "), got " + list(t.sizes()));
+        // (It has no storage, and the library would take it for no table.)
+        if (nseq > 0 && t.size(1) < 1)
+            value_error(std::string(name) + " must have at least one column, got " + list(t.sizes()));
         *seq_stride = t.stride(0);
         *step_stride = t.stride(1);
         return t.size(1);
@@ -143,8 +146,6 @@ PyObject* attention(PyObject* const* arg) {
         if (read && widths[1] && read != widths[1])
             value_error("read and write tables have different widths " + std::to_string(read) +
                         " and " + std::to_string(widths[1]));
-        if ((accepted.defined() || dst.defined()) && a.steps < 1 && a.nseq > 0)
-            value_error("slot tables must have at least one column");
         if (a.steps < 1 && (accepted.defined() || dst.defined())) a.steps = 1;
     } else {
         sequences(a, cu, has, slots, a.rows, a.nslots, device);

@@ -1,5 +1,6 @@
-"""include/attention.h called directly, where the Python binding refuses a call that the header
-allows."""
+"""Slots of linear attention where they are left out or their tables are empty: include/attention.h
+called directly, where the Python binding refuses a call that the header allows, and the
+binding's refusals."""
 import ctypes
 
 import pytest
@@ -59,3 +60,33 @@ def test_sequences_past_the_slots_are_inert(entry, rows_of_each, delta):
     assert same(out[:kept], want[:kept]) and out[kept:].isnan().all()
     assert not out[:kept].isnan().any()
     assert same(state, want_state) and same(state[nslots:], start[nslots:])
+
+
+@pytest.mark.parametrize("dst", [False, True])
+@pytest.mark.parametrize("accepted", [False, True])
+@pytest.mark.parametrize("slots", [False, True])
+def test_tables_without_columns_are_refused(slots, accepted, dst):
+    """Not taken for tables that are left out."""
+    if not (slots or dst):
+        return
+    q, v, decay = torch.zeros(2, 1, 64, device=DEV), torch.zeros(2, 1, 32, device=DEV), torch.zeros(1, device=DEV)
+    state = torch.zeros(2, 1, 32, 64, device=DEV)
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV)
+    table = torch.zeros(2, 3, dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError, match="at least one column"):
+        ssu.linear_attention_packed(
+            state, q, q, v, decay, cu, state_batch_indices=table[:, :0] if slots else table,
+            num_accepted_tokens=torch.ones(2, dtype=torch.int32, device=DEV) if accepted else None,
+            dst_state_batch_indices=table[:, :0] if dst else None)
+    assert not state.any()
+
+
+def test_empty_tables_of_no_sequences():
+    """Nothing to do is no error."""
+    q, v = torch.zeros(0, 1, 64, device=DEV), torch.zeros(0, 1, 32, device=DEV)
+    table = torch.zeros(0, 0, dtype=torch.int32, device=DEV)
+    out = ssu.linear_attention_packed(
+        torch.zeros(2, 1, 32, 64, device=DEV), q, q, v, torch.zeros(1, device=DEV),
+        torch.zeros(1, dtype=torch.int32, device=DEV), state_batch_indices=table,
+        num_accepted_tokens=torch.zeros(0, dtype=torch.int32, device=DEV), dst_state_batch_indices=table)
+    assert out.shape == (0, 1, 32)
