@@ -37,7 +37,7 @@ extern "C" {
  * [0, vocab) is rejected; where no token has any weight, next is -1. NaN scores count as minus
  * infinity. Probabilities from scores (accurate to 2^-40) and sums are fp64.
  * A range that is empty, longer than window + 1, outside [0, rows] or running backwards:
- * tokens -1, num_accepted 0.
+ * tokens -1, num_accepted 0; the other sequences are those of their own ranges, also where these overlap.
  */
 typedef struct ssu_verify_args {
     uint32_t struct_size;      /* sizeof(ssu_verify_args) */

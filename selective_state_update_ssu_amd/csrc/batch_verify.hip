@@ -60,6 +60,7 @@ struct VerifyParams {
     int32_t* tokens;
     int32_t* num_accepted;
     Stats* stats;   // [rows, tiles]
+    int32_t* owner; // [rows]: the sequence with whose temperature a row's statistics were taken, -1: none
     double* sums;   // [nseq, tiles, 2]: of w, of p
     Choice* choice; // [nseq]
     int64_t target_stride, rows, nseq, window;
@@ -168,7 +169,8 @@ __device__ __forceinline__ Stats merge(Stats a, Stats b, double c) {
 
 // ------------------------------------------------------------- statistics of scores
 
-// A row's sequence is found from cu_seqlens (its temperature is needed).
+// A row's sequence is found from cu_seqlens (its temperature is needed), by bisection: where a range
+// runs backwards it can find another one than the range's own, which is why it is noted.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void stats_kernel(const VerifyParams p) {
     constexpr int E = seg_elements<T>();
@@ -181,7 +183,9 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(const VerifyParams p) {
 #pragma unroll
     for (int s = 0; s < kSegs; ++s) load_seg<T>(row, base + s * kThreads * E, p.vocab, f[s], -INFINITY);
     const int64_t b = count_starts(p.cu, p.cu64, p.nseq + 1, r) - 1;
-    if (b < 0 || b >= p.nseq) return;
+    const bool owned = b >= 0 && b < p.nseq;
+    if (tile == 0 && threadIdx.x == 0) p.owner[r] = owned ? static_cast<int32_t>(b) : -1;
+    if (!owned) return;
     const float temperature = p.temperature[b];
     float most = -INFINITY;  // NaN counts as minus infinity
 #pragma unroll
@@ -233,6 +237,52 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(const VerifyParams p) {
 // Statistics of a row of scores, taken by kLanes neighbouring lanes that share its tiles; each gets
 // the whole.
 constexpr int kLanes = 8;
+
+// The larger of two scores and the first token that has it, over the lanes.
+__device__ __forceinline__ void first_largest(float& most, int& first) {
+#pragma unroll
+    for (int d = 1; d < kLanes; d *= 2) {
+        const float other = __shfl_xor(most, d);
+        const int at = __shfl_xor(first, d);
+        if (other > most || (other == most && at < first)) {
+            most = other;
+            first = at;
+        }
+    }
+}
+
+__device__ __forceinline__ void complete(Row& row, float most, int first, double sum) {
+#pragma unroll
+    for (int d = 1; d < kLanes; d *= 2) sum += __shfl_xor(sum, d);
+    row.most = most;
+    row.first = first == INT_MAX ? 0 : first;
+    row.inverse = 1. / sum;
+}
+
+// The same from the row itself: for rows whose statistics were taken for another sequence, which only
+// happens beside a range that runs backwards.
+template <typename T>
+__device__ __forceinline__ void row_anew(const VerifyParams& p, int64_t r, Row& row) {
+    const T* from = static_cast<const T*>(p.target) + r * p.target_stride;
+    const int lane = threadIdx.x % kLanes;
+    float most = -INFINITY;
+    int first = INT_MAX;
+    for (int64_t x = lane; x < p.vocab; x += kLanes) {
+        const float score = static_cast<float>(from[x]);
+        if (score > most) {
+            most = score;
+            first = static_cast<int>(x);
+        }
+    }
+    first_largest(most, first);
+    double sum = 0.;
+    if (row.temperature > 0.f && most > -INFINITY)
+        for (int64_t x = lane; x < p.vocab; x += kLanes)
+            sum += weight_of(static_cast<float>(from[x]), most, row.c);
+    complete(row, most, first, sum);
+}
+
+template <typename T>
 __device__ __forceinline__ Row row_stats(const VerifyParams& p, int64_t b, int64_t r) {
     Row row = {0.f, 1.f, 0, 0., 1.};
     if (!p.temperature) return row;
@@ -249,15 +299,7 @@ __device__ __forceinline__ Row row_stats(const VerifyParams& p, int64_t b, int64
             first = s.first;  // of equal ones the first tile's
         }
     }
-#pragma unroll
-    for (int d = 1; d < kLanes; d *= 2) {
-        const float other = __shfl_xor(most, d);
-        const int at = __shfl_xor(first, d);
-        if (other > most || (other == most && at < first)) {
-            most = other;
-            first = at;
-        }
-    }
+    first_largest(most, first);
     double sum = 0.;
     if (row.temperature > 0.f) {
         for (int t = lane; t < p.tiles; t += kLanes) {
@@ -267,11 +309,8 @@ __device__ __forceinline__ Row row_stats(const VerifyParams& p, int64_t b, int64
                        (s.most == most ? 1. : exp2_of((static_cast<double>(s.most) - most) * row.c));
         }
     }
-#pragma unroll
-    for (int d = 1; d < kLanes; d *= 2) sum += __shfl_xor(sum, d);
-    row.most = most;
-    row.first = first == INT_MAX ? 0 : first;
-    row.inverse = 1. / sum;
+    complete(row, most, first, sum);
+    if (p.owner[r] != b) row_anew<T>(p, r, row);
     return row;
 }
 
@@ -314,7 +353,7 @@ __device__ __forceinline__ Choice choice_of(const VerifyParams& p, int64_t b, in
                                  b * p.probs_seq_stride + i * p.probs_step_stride + x);
                 u = static_cast<double>(p.uniforms[b * p.uniform_stride + i]);
             }
-            c.row = row_stats(p, b, r);
+            c.row = row_stats<T>(p, b, r);
             taken = token && u * q < chance(p, c.row, value, static_cast<int>(x));
         }
         const unsigned long long missed = ~__ballot(taken);
@@ -584,6 +623,7 @@ int64_t round_up(int64_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 int64_t stats_bytes(int64_t rows, int64_t vocab, bool scores) {
     return scores ? round_up(rows * tiles_of(vocab, 4) * static_cast<int64_t>(sizeof(Stats))) : 0;
 }
+int64_t owner_bytes(int64_t rows, bool scores) { return scores ? round_up(rows * 4) : 0; }
 int64_t sums_bytes(int64_t nseq, int64_t vocab) { return round_up(nseq * tiles_of(vocab, 4) * 16); }
 
 int check(const ssu_verify_args* a) {
@@ -687,8 +727,8 @@ extern "C" {
 
 size_t ssu_verify_workspace_bytes(int64_t rows, int64_t nseq, int64_t vocab, int32_t scores) {
     if (rows < 0 || nseq < 0 || vocab < 1) return 0;
-    return static_cast<size_t>(stats_bytes(rows, vocab, scores != 0) + sums_bytes(nseq, vocab) +
-                               nseq * static_cast<int64_t>(sizeof(Choice)));
+    return static_cast<size_t>(stats_bytes(rows, vocab, scores != 0) + owner_bytes(rows, scores != 0) +
+                               sums_bytes(nseq, vocab) + nseq * static_cast<int64_t>(sizeof(Choice)));
 }
 
 int ssu_verify_drafts(const ssu_verify_args* a, void* stream) {
@@ -706,6 +746,8 @@ int ssu_verify_drafts(const ssu_verify_args* a, void* stream) {
     char* ws = static_cast<char*>(a->workspace);
     p.stats = reinterpret_cast<Stats*>(ws);
     ws += stats_bytes(a->rows, a->vocab, a->temperature != nullptr);
+    p.owner = reinterpret_cast<int32_t*>(ws);
+    ws += owner_bytes(a->rows, a->temperature != nullptr);
     p.sums = reinterpret_cast<double*>(ws);
     p.choice = reinterpret_cast<Choice*>(ws + sums_bytes(a->nseq, a->vocab));
     p.target_stride = a->target_stride;
