@@ -33,9 +33,10 @@ extern "C" {
  * sequence whose states stand. With temperature, target holds scores: p = softmax(score /
  * temperature[b]), and where temperature[b] is 0 or below, one at the largest score (the
  * lowest token of equal ones). Without it target holds probabilities, which need not sum to one.
- * Probabilities and weights that are not above 0 (NaN among them) count as 0; a draft outside
- * [0, vocab) is rejected; where no token has any weight, next is -1. NaN scores count as minus
- * infinity. Probabilities from scores (accurate to 2^-40) and sums are fp64.
+ * Probabilities p that are not above 0 (NaN among them) and q below 0 count as 0. A q of NaN
+ * rejects its draft and leaves its token out of w; a draft outside [0, vocab) is rejected; where no
+ * token has any weight, next is -1. NaN scores count as minus infinity. Probabilities from scores
+ * (accurate to 2^-40) and sums are fp64.
  * A range that is empty, longer than window + 1, outside [0, rows] or running backwards:
  * tokens -1, num_accepted 0; the other sequences are those of their own ranges, also where these overlap.
  */

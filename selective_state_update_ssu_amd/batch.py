@@ -44,9 +44,10 @@ def verify_drafts(target, draft_tokens, uniforms, cu_seqlens, *, draft_probs=Non
 
     target holds probabilities, or with temperature (fp32 [sequences]) scores: p = softmax(score
     / temperature), and where the temperature is 0 or below, one at the largest score (the
-    lowest token of equal ones). Probabilities and weights that are not above 0, NaN among them,
-    count as 0, NaN scores as minus infinity; a draft outside the vocabulary is rejected; where
-    no token has any weight the drawn one is -1. A sequence without rows, with more than window
+    lowest token of equal ones). Probabilities p that are not above 0, NaN among them, and q below 0
+    count as 0, NaN scores as minus infinity; a q of NaN rejects its draft and leaves its token out of
+    the draw; a draft outside the vocabulary is rejected; where no token has any weight the drawn one
+    is -1. A sequence without rows, with more than window
     + 1 or with rows outside the target gets tokens -1 and num_accepted 0."""
     return _run("verify", stream, target, draft_tokens, uniforms, cu_seqlens, draft_probs,
                 temperature, workspace)

@@ -351,6 +351,7 @@ __device__ __forceinline__ Choice choice_of(const VerifyParams& p, int64_t b, in
                 if (p.probs)
                     q = value_of(p.probs, p.probs_dtype,
                                  b * p.probs_seq_stride + i * p.probs_step_stride + x);
+                if (q < 0.f) q = 0.f;  // (NaN stays, and rejects)
                 u = static_cast<double>(p.uniforms[b * p.uniform_stride + i]);
             }
             c.row = row_stats<T>(p, b, r);
@@ -427,8 +428,8 @@ struct Draw {
         }
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            const double left = full[i] - static_cast<double>(q[i]);
-            w[i] = left > 0. ? left : 0.;  // NaN counts as 0
+            const double left = full[i] - static_cast<double>(q[i] < 0.f ? 0.f : q[i]);
+            w[i] = left > 0. ? left : 0.;  // of NaN: 0
         }
     }
 };
