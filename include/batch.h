@@ -36,7 +36,7 @@ extern "C" {
  * Probabilities p that are not above 0 (NaN among them) and q below 0 count as 0. A q of NaN
  * rejects its draft and leaves its token out of w; a draft outside [0, vocab) is rejected; where no
  * token has any weight, next is -1. NaN scores count as minus infinity. Probabilities from scores
- * (accurate to 2^-40) and sums are fp64.
+ * (accurate to 2^-37) and sums are fp64.
  * A range that is empty, longer than window + 1, outside [0, rows] or running backwards:
  * tokens -1, num_accepted 0; the other sequences are those of their own ranges, also where these overlap.
  */
