@@ -434,21 +434,21 @@ void chunk_kernel(const Params p) {
         const unsigned col = v0 + wv + 16 * c + of_lane % 16, key = 16 * t + 4 * (of_lane / 16);
         return key < static_cast<unsigned>(p.K) ? col * p.K + key : kOutOfRange / 4;
     };
-    of_dtype(dtype, [&](auto type) {
-        const Rsrc from = range_of(enter, has ? p.V * p.K * in_size : 0);
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
+    for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int t = 0; t < KT; ++t) S[c][t] = load4<decltype(type)>(from, place(lane, c, t));
-    });
-    if (!OUT && !values)
+        for (int t = 0; t < KT; ++t)
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
+            for (int i = 0; i < 4; ++i)
+                S[c][t][i] = !OUT && !values && 16 * t + 4 * g + i == v0 + wv + 16 * c + l16 ? 1.f : 0.f;
+    if (has)
+        of_dtype(dtype, [&](auto type) {
+            const Rsrc from = range_of(enter, p.V * p.K * in_size);
 #pragma unroll
-            for (int t = 0; t < KT; ++t)
+            for (int c = 0; c < NC; ++c)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    S[c][t][i] = 16 * t + 4 * g + i == v0 + wv + 16 * c + l16 ? 1.f : 0.f;
+                for (int t = 0; t < KT; ++t) S[c][t] = load4<decltype(type)>(from, place(lane, c, t));
+        });
 
     // ---- what a thread moves of a chunk: its segments of q, k and v, one row's decay and beta.
     // Segment i lies QROWS (VROWS) rows behind segment i - 1, in the same columns.
