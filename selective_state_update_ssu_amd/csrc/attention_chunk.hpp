@@ -1090,11 +1090,16 @@ hipError_t launch_passes(const Params& p, hipStream_t stream) {
         const hipError_t e = launch_ends<IT, KP, DELTA, WIDE>(p, stream);
         if (e != hipSuccess) return e;
     }
-    // Slices of 128 columns read q, k and P half as often: 2.8 us against 3.1 for 64 rows x 64
-    // columns on a full card (delta rule 4.2 against 4.9), though these have four waves per SIMD. Where workgroups are few, or registers
-    // are (inputs of several parts, keys of more than 128), slices of 64.
+    // Slices of 128 columns read q, k and P half as often; those of 64 are twice as many, and those of
+    // the plain form have four waves per SIMD instead of two. From four of 64 per compute unit on the
+    // wide ones gain (bf16, heads of 128 x 128; us with 64 and 128, delta rule behind: 64 of 250 rows
+    // 17.2 and 23.4, 28.3 and 38.9; 512 of 64 rows 11.9 and 12.6, 16.3 and 17.1; 768 of 250 rows 33.8
+    // and 38.7, 61.8 and 60.7; 1,024 of 128 rows 26.1 and 25.6, 46.7 and 38.5; 4,096 of 250 rows
+    // 183 and 168, 312 and 246). Where registers are few (inputs of several parts, keys of more than
+    // 128), slices of 64.
     if constexpr (std::is_same<IT, __bf16>::value && KP <= 128 && WIDE)
-        if (p.piece == 0 && p.V > 64) return launch_out<IT, KP, 2, DELTA, WIDE>(p, stream);
+        if (p.piece == 0 && p.V > 64 && p.nseq * p.nheads * ((p.V + 63) / 64) >= 1024)
+            return launch_out<IT, KP, 2, DELTA, WIDE>(p, stream);
     return launch_out<IT, KP, 1, DELTA, WIDE>(p, stream);
 }
 
