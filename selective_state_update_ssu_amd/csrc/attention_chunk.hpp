@@ -613,7 +613,7 @@ void chunk_kernel(const Params p) {
             for (int t = 0; t < NO; ++t)
                 *reinterpret_cast<u32x2*>(&lds.p[t][Shape::p_at(l16, 8 * g + 4)]) = u32x2{0, 0};
 
-    float total = 0.f;  // decay of the piece, as an exponent of 2
+    double total = 0.;  // decay of the piece, as an exponent of 2
     load(0);
     for (int64_t first = 0; first < n_all; first += C) {
         const int n = static_cast<int>(n_all - first < C ? n_all - first : C);
@@ -826,7 +826,8 @@ void chunk_kernel(const Params p) {
 
             // S = e^(G_C) S + k^T (weighted R).
             const float egc = lds.eg[C - 1];
-            if constexpr (!OUT && !DELTA) total += lds.gh[C - 1];
+            if constexpr (!OUT && !DELTA)
+                total += static_cast<double>(lds.gh[C - 1]) + static_cast<double>(lds.gl[C - 1]);
             u32x4 wr[NC][TB][3];
 #pragma unroll
             for (int t = 0; t < CT; ++t) {
@@ -899,7 +900,11 @@ void chunk_kernel(const Params p) {
     else
         leave(values ? p.ends + in_ends : p.moves + (pi * p.nheads + h) * p.K * p.K, float());
     if constexpr (!OUT && !DELTA)
-        if (tid == 0 && slice == 0) p.sums[pi * p.nheads + h] = __builtin_amdgcn_exp2f(total);
+        if (tid == 0 && slice == 0) {
+            // 2^(hi + lo), lo below half a step of hi: 2^hi (1 + lo log(2)).
+            const float hi = static_cast<float>(total), e = __builtin_amdgcn_exp2f(hi);
+            p.sums[pi * p.nheads + h] = fmaf(e, static_cast<float>(total - hi) * layer::kLn2, e);
+        }
 }
 
 // The states that enter the pieces of a sequence: ends[j] becomes M_j ends[j - 1] + ends[j] for

@@ -176,3 +176,27 @@ def test_the_same_call_gives_the_same_bits(delta, io, K, V, heads, nseq, most):
         if found is None:
             found = out, state
         assert same(out, found[0]) and same(state, found[1])
+
+
+@pytest.mark.gpu
+def test_decays_of_long_pieces():
+    """Without values a state is its entering one times a decay, through 12 pieces of 960 rows and one
+    of a single row. Its error: 30 chunks of the first piece, each an exponential (one step of fp32,
+    2^-23, which also covers the half step of its small argument) and a product (half a step); for each
+    of 11 pieces an exponential (a step), its correction, and the product and sum that join (half a
+    step each), 2.5 steps; the last chunk like one of the first; half a step when the state is stored,
+    which is fp32 anyway."""
+    piece, heads, K, V = 960, 80, 64, 64
+    rows = 12 * piece + 1
+    assert -(-(-(-rows * heads // 1024)) // 64) * 64 == piece  # the length that a call of these sizes cuts at
+    d = Draw(9)
+    decay = -(0.5 + torch.arange(heads) / (2 * heads)) * 60 / rows
+    start = d.uniform(1.0, 2.0, 1, heads, V, K)
+    q, k = (torch.nn.functional.normalize(d.normal(rows, heads, K), dim=-1).to(DEV) for _ in range(2))
+    state = start.to(DEV)
+    ssu.linear_attention_varlen(state, q, k, torch.zeros(rows, heads, V, device=DEV), decay.to(DEV),
+                                torch.tensor([0, rows], dtype=torch.int32, device=DEV),
+                                has_initial_state=torch.ones(1, dtype=torch.bool, device=DEV))
+    want = start.double() * torch.exp(decay.double() * rows)[None, :, None, None]
+    steps = 31 * 1.5 + 11 * 2.5 + 0.5
+    assert float((state.cpu().double() / want - 1).abs().max()) < steps * 2.0 ** -23
