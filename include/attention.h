@@ -19,8 +19,8 @@
  * rows, but for decays of minus infinity, which forget the state.
  *
  *   ssu_attention_varlen   packed prompts, by chunks on the matrix cores; numbers enter products
- *                          as bf16 parts, so that what reaches the state is accurate to about
- *                          2^-23 of the magnitudes in it, what reaches only a 16-bit out to 2^-16
+ *                          as bf16 parts, accurate to about 2^-23 of the magnitudes, but for the
+ *                          state that meets q on the way to a 16-bit out: to 2^-17
  *   ssu_attention_update   one row per sequence, fp32 arithmetic
  *   ssu_attention_packed   a few rows per sequence, a state stored after each (windows of
  *                          drafted tokens), slots through tables as in ssu_packed_varlen

@@ -22,11 +22,14 @@
 // it M is what it makes of the identity as a state with no values, walked as further value columns.
 //
 // Precision: the matrix cores take bf16, so a number goes in as parts of 8 bits: bf16 inputs as
-// one (exactly), fp16 as two (exactly), fp32 as three; what is derived and reaches the state (S,
-// the weighted R) as three, which holds fp32's 24 bits; what only reaches out as two, three for
-// fp32. Products of parts whose places add up to the last part's or less are summed: what is left
-// out is 2^-23 of the magnitudes, for out in 16 bits 2^-16. The triangular blocks go through the
-// fp32 matrix instruction.
+// one (exactly), fp16 as two (exactly), fp32 as three; what is derived (S, P, R, the weighted R) as
+// three, which holds fp32's 24 bits. Products of parts whose places add up to the third's or less are
+// summed: what is left out is 2^-23 of the magnitudes. Only the S that q meets goes to out in 16 bits
+// as two: 2^-17 of |S| |q| is left out, where out keeps 2^-9 or 2^-12. (Three parts there as well: one
+// prompt of 32,768 rows 745 us instead of 556, whose kernel has no registers left; the delta rule,
+// whose S is in three anyway, 3 % more. P and R in two as well: 540 us and 3 % less, and four times as
+// many values of out that fp32 arithmetic rounds to the other side.) The triangular blocks go through
+// the fp32 matrix instruction.
 //
 // Layouts (16x16 tiles, lane l, g = l / 16): an operand has the outer index at l % 16 and
 // contracted indices in its registers, a result D[m][n] has n at l % 16 and m = 4 g + i in
@@ -203,8 +206,8 @@ template <typename IT, int KP, int NC, bool DELTA, Pass PASS>
 struct ChunkShape {
     static constexpr bool OUT = PASS == kOut;
     static constexpr int NI = std::is_same<IT, float>::value ? 3 : std::is_same<IT, _Float16>::value ? 2 : 1;
-    static constexpr int NO = NI == 3 ? 3 : 2;                     // parts of what reaches out only
-    static constexpr int NS = DELTA ? 3 : NO;                      // parts of S
+    static constexpr int NP = 3;                                   // parts of P, with the delta rule of R
+    static constexpr int NS = NI == 3 || DELTA ? 3 : 2;            // parts of S
     static constexpr int C = 32;                                   // rows of a chunk
     static constexpr int VW = 64 * NC;                             // columns of a slice
     static constexpr int CT = C / 16, KT = KP / 16, KB = KP / 32, TB = C / 32;
@@ -218,7 +221,7 @@ struct ChunkShape {
     static constexpr int VS = VW + 8, PS = C + 8, AS = 20, TILE = 16 * AS;
     struct Lds {
         unsigned short k[NI][C][KP], v[NI][C][VS];
-        unsigned short q[OUT ? NI : 1][OUT ? C : 1][OUT ? KP : 8], p[OUT ? NO : 1][OUT ? C * PS : 8];
+        unsigned short q[OUT ? NI : 1][OUT ? C : 1][OUT ? KP : 8], p[OUT ? NP : 1][OUT ? C * PS : 8];
         float gh[C], gl[C], eg[C], ew[C], beta[C];
         float a[DELTA ? CT * (CT + 1) / 2 * TILE : 4];
     };
@@ -362,7 +365,7 @@ __global__ __launch_bounds__(kChunkThreads, (ChunkShape<IT, KP, NC, DELTA, PASS>
 void chunk_kernel(const Params p) {
     typedef ChunkShape<IT, KP, NC, DELTA, PASS> Shape;
     constexpr bool OUT = PASS == kOut;
-    constexpr int NI = Shape::NI, NO = Shape::NO, NS = Shape::NS, C = Shape::C, CT = Shape::CT,
+    constexpr int NI = Shape::NI, NP = Shape::NP, NS = Shape::NS, C = Shape::C, CT = Shape::CT,
                   KT = Shape::KT, KB = Shape::KB, TB = Shape::TB, VW = Shape::VW;
     constexpr int QSEGS = C * KP / 8 / kChunkThreads, VSEGS = C * VW / 8 / kChunkThreads;
     constexpr int QROWS = kChunkThreads / (KP / 8), VROWS = kChunkThreads / (VW / 8);
@@ -596,11 +599,11 @@ void chunk_kernel(const Params p) {
             if constexpr (DELTA) a[r] = ahead > r ? -beta * (a[r] * e) : 0.f;
         }
         if constexpr (OUT) {
-            u32x2 part[NO];
+            u32x2 part[NP];
             split4(s, part);
             const int to = Shape::p_at(i, 32 * (jt / 2) + 8 * g + 4 * (jt % 2));
 #pragma unroll
-            for (int t = 0; t < NO; ++t) *reinterpret_cast<u32x2*>(&lds.p[t][to]) = part[t];
+            for (int t = 0; t < NP; ++t) *reinterpret_cast<u32x2*>(&lds.p[t][to]) = part[t];
         }
         if constexpr (DELTA)
             *reinterpret_cast<f32x4*>(&lds.a[Shape::a_at(it, jt) + l16 * Shape::AS + 4 * g]) = a;
@@ -610,7 +613,7 @@ void chunk_kernel(const Params p) {
     if constexpr (OUT)
         if (wave == 0)
 #pragma unroll
-            for (int t = 0; t < NO; ++t)
+            for (int t = 0; t < NP; ++t)
                 *reinterpret_cast<u32x2*>(&lds.p[t][Shape::p_at(l16, 8 * g + 4)]) = u32x2{0, 0};
 
     double total = 0.;  // decay of the piece, as an exponent of 2
@@ -692,7 +695,7 @@ void chunk_kernel(const Params p) {
                 for (int i = 0; i < NS; ++i)
 #pragma unroll
                     for (int j = 0; j < NI; ++j) {
-                        constexpr int last = of_k ? 2 : NO - 1;
+                        constexpr int last = of_k || NI == 3 ? 2 : 1;
                         if (i + j > last) continue;
 #pragma unroll
                         for (int t = 0; t < CT; ++t)
@@ -707,7 +710,7 @@ void chunk_kernel(const Params p) {
             });
 
             // R as an operand over the chunk's rows: v as it is, or the solution.
-            constexpr int NR = DELTA ? NO : NI;
+            constexpr int NR = DELTA ? NP : NI;
             u32x4 R[NC][TB][NR];
 #pragma unroll
             for (int t = 0; t < CT; ++t) {
@@ -764,14 +767,16 @@ void chunk_kernel(const Params p) {
             }
 
             if constexpr (OUT) {
-                u32x4 pf[2][TB][NO];
+                // Where four waves share a SIMD's registers P's last part is read when the others are in use.
+                constexpr int AHEAD = Shape::waves(WIDE) == 4 ? NP - 1 : NP;
+                u32x4 pf[2][TB][AHEAD];
                 float pe[2];
                 const auto fetch_p = [&](int t) {
                     pe[t % 2] = lds.eg[16 * t + l16];
 #pragma unroll
                     for (int x = 0; x <= t / 2; ++x)
 #pragma unroll
-                        for (int y = 0; y < NO; ++y)
+                        for (int y = 0; y < AHEAD; ++y)
                             pf[t % 2][x][y] = read16(&lds.p[y][Shape::p_at(16 * t + l16, 32 * x + 8 * g)]);
                 };
                 fetch_p(0);
@@ -784,8 +789,15 @@ void chunk_kernel(const Params p) {
                         O[t][c] *= pe[t % 2];
 #pragma unroll
                         for (int x = 0; x <= t / 2; ++x)
-                            O[t][c] = mma_parts<NO - 1>(R[c][x], pf[t % 2][x], O[t][c]);
+                            O[t][c] = mma_parts<2>(R[c][x], pf[t % 2][x], O[t][c]);
                     }
+                    if constexpr (AHEAD < NP)
+#pragma unroll
+                        for (int x = 0; x <= t / 2; ++x) {
+                            const u32x4 rest = read16(&lds.p[NP - 1][Shape::p_at(16 * t + l16, 32 * x + 8 * g)]);
+#pragma unroll
+                            for (int c = 0; c < NC; ++c) O[t][c] = mma(R[c][x][0], rest, O[t][c]);
+                        }
                 });
                 if constexpr (WIDE) {
                     const Rsrc ro = range_of(out, n * os);
