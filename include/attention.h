@@ -16,7 +16,9 @@
  * 2023, for the decay; Yang et al., "Gated Delta Networks", 2024, for the delta rule.)
  * States and sums are fp32; the state is rounded once to nearest when it is stored, out
  * once when it is written. q, k, v and the decays must be finite where a sequence has
- * rows, but for decays of minus infinity, which forget the state.
+ * rows, but for decays of minus infinity, which forget the state. An infinity or NaN in a row of the
+ * state makes what that row gives infinite or NaN (not always the one of the two that the formula
+ * has), and nothing else.
  *
  *   ssu_attention_varlen   packed prompts, by chunks on the matrix cores; numbers enter products
  *                          as bf16 parts, accurate to about 2^-23 of the magnitudes, but for the

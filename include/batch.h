@@ -45,7 +45,7 @@ typedef struct ssu_verify_args {
     int32_t target_dtype;      /* ssu_dtype */
     const void *target;        /* [rows, vocab], a row's values adjacent */
     int64_t target_stride;     /* elements between rows, >= 0 */
-    int64_t rows, vocab;       /* >= 0; 1 to 2^31 - 1 */
+    int64_t rows, vocab;       /* >= 0, < 2^31; 1 to 2^31 - 2^20 - 1 */
     int64_t nseq, window;      /* >= 0; >= 0, < 2^20 */
     const void *cu_seqlens;    /* [nseq + 1] */
     int32_t cu_dtype;          /* ssu_index_dtype */

@@ -17,7 +17,8 @@ int64_t round_up(int64_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 // How a call's sequences are cut, and its scratch. A workgroup walks one head of a piece, 64 columns
 // of values, and two to four of them share a compute unit: sequences that give fewer than 512
-// are cut, towards 1,024 of them. (One prompt of 32,768 rows, 80 heads of 128 x 64 in bf16: 1,700 us
+// are cut, towards 1,024 of them, however unequal they are: a long prompt beside enough short ones is
+// not. (One prompt of 32,768 rows, 80 heads of 128 x 64 in bf16, when this was chosen: 1,700 us
 // uncut, 631 for 480 wanted, 580 for 1,024, 565 for 2,048.) A piece costs two more walks of its
 // rows for the state, with the delta rule four and a product of matrices: short ones are
 // not worth it. (4,096 rows through the delta rule, 32 heads of 128 x 128 in fp16: 508 us

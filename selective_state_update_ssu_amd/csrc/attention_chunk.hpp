@@ -26,10 +26,10 @@
 // three, which holds fp32's 24 bits. Products of parts whose places add up to the third's or less are
 // summed: what is left out is 2^-23 of the magnitudes. Only the S that q meets goes to out in 16 bits
 // as two: 2^-17 of |S| |q| is left out, where out keeps 2^-9 or 2^-12. (Three parts there as well: one
-// prompt of 32,768 rows 745 us instead of 556, whose kernel has no registers left; the delta rule,
-// whose S is in three anyway, 3 % more. P and R in two as well: 540 us and 3 % less, and four times as
-// many values of out that fp32 arithmetic rounds to the other side.) The triangular blocks go through
-// the fp32 matrix instruction.
+// prompt of 32,768 rows 782 us instead of 556, since its kernel has no registers left; the delta rule,
+// whose S is in three anyway, 2 % more. P and R in two as well: 544 us, with the delta rule 16 prompts
+// 298 instead of 309, and four times as many values of out that fp32 arithmetic rounds to the other
+// side.) The triangular blocks go through the fp32 matrix instruction.
 //
 // Layouts (16x16 tiles, lane l, g = l / 16): an operand has the outer index at l % 16 and
 // contracted indices in its registers, a result D[m][n] has n at l % 16 and m = 4 g + i in
@@ -43,13 +43,13 @@
 // Chunks of 32 rows: with 64 the triangular part doubles per row and P, A and the rows of
 // two chunks (one in use, one on its way in registers) leave fewer waves; it measured no
 // faster, and slower with the delta rule. What bounds it is the issue of instructions: per chunk
-// and wave about 580 vector instructions for 92 matrix ones, a third of them the splitting of S,
+// and wave about 590 vector instructions for 95 matrix ones, a third of them the splitting of S,
 // which every chunk needs anew. 16 prompts of 17,885 rows, 32 heads of 128 x 128 in bf16 with fp32
-// states: 180-200 us (3.3-3.6 TB/s of the 655 MB that have to move; the vector units 38 % busy, matrix
-// cores 24 %, LDS 19 %, and the longest prompt's workgroups outlast the rest: 1.3 waves of 2
-// per SIMD on average), with the delta rule 286-319 us (40 %, 30 %, 18 %). One prompt of 32,768
-// rows, 80 heads of 128 x 64: 531-580 us (a quarter of it the ends of pieces); one of 4,096 rows
-// through the delta rule in fp16: 245 us (half of it the ends).
+// states: 186-200 us (3.3-3.5 TB/s of the 655 MB that have to move; the vector units 40 % busy, matrix
+// cores 25 %, LDS 20 %, and the longest prompt's workgroups outlast the rest: 1.3 waves of 2
+// per SIMD on average), with the delta rule 299-318 us (40 %, 31 %, 18 %). One prompt of 32,768
+// rows, 80 heads of 128 x 64: 556-560 us (a quarter of it the ends of pieces); one of 4,096 rows
+// through the delta rule in fp16: 252 us (half of it the ends).
 #pragma once
 
 #include <type_traits>

@@ -8,9 +8,11 @@
 // definition has it; their order is fixed. (One workgroup per sequence for the second and third
 // launch: 84 us instead of 40 for 128 sequences of 131,072 tokens, and no faster for four.)
 //
-// fp64 instructions bound the first two as much as memory: 17 per score. 128 sequences of
-// 131,072 tokens, windows of up to 4 drafts, bf16 scores: 79 us (42 + 30 + 10 under the profiler) for
-// 134 MB of scores; 4 sequences of 32,000 tokens, probabilities in fp32: 11 us, two launches.
+// 128 sequences of 131,072 tokens, windows of up to 4 drafts, bf16 scores: 80-82 us (42 + 31 + 11 under
+// the profiler) for 134 MB of scores. The first launch takes 17 fp64 instructions per score, about half
+// of its time, and its bytes the other half (vector units 61 % busy). The second has a third of that
+// work: its waves wait, two per SIMD, for the dependent reads that find the row before they
+// load any of it (40 % busy). 4 sequences of 32,000 tokens, probabilities in fp32: 11 us, two launches.
 #include "batch.h"
 #include "layer_common.hpp"
 
