@@ -45,11 +45,11 @@
 // faster, and slower with the delta rule. What bounds it is the issue of instructions: per chunk
 // and wave about 590 vector instructions for 95 matrix ones, a third of them the splitting of S,
 // which every chunk needs anew. 16 prompts of 17,885 rows, 32 heads of 128 x 128 in bf16 with fp32
-// states: 186-200 us (3.3-3.5 TB/s of the 655 MB that have to move; the vector units 40 % busy, matrix
+// states: 184-202 us (3.2-3.6 TB/s of the 655 MB that have to move; the vector units 40 % busy, matrix
 // cores 25 %, LDS 20 %, and the longest prompt's workgroups outlast the rest: 1.3 waves of 2
-// per SIMD on average), with the delta rule 299-318 us (40 %, 31 %, 18 %). One prompt of 32,768
-// rows, 80 heads of 128 x 64: 556-560 us (a quarter of it the ends of pieces); one of 4,096 rows
-// through the delta rule in fp16: 252 us (half of it the ends).
+// per SIMD on average), with the delta rule 296-318 us (40 %, 31 %, 18 %). One prompt of 32,768
+// rows, 80 heads of 128 x 64: 556-574 us (a quarter of it the ends of pieces); one of 4,096 rows
+// through the delta rule in fp16: 250 us (half of it the ends).
 #pragma once
 
 #include <type_traits>
@@ -767,17 +767,21 @@ void chunk_kernel(const Params p) {
             }
 
             if constexpr (OUT) {
-                // Where four waves share a SIMD's registers P's last part is read when the others are in use.
-                constexpr int AHEAD = Shape::waves(WIDE) == 4 ? NP - 1 : NP;
-                u32x4 pf[2][TB][AHEAD];
+                // P's last part comes last; where four waves share a SIMD's registers it is read only then.
+                constexpr bool LATE = Shape::waves(WIDE) == 4;
+                u32x4 pf[2][TB][NP - 1], rest[2][TB];
                 float pe[2];
+                const auto read_p = [&](int t, int x, int part) {
+                    return read16(&lds.p[part][Shape::p_at(16 * t + l16, 32 * x + 8 * g)]);
+                };
                 const auto fetch_p = [&](int t) {
                     pe[t % 2] = lds.eg[16 * t + l16];
 #pragma unroll
-                    for (int x = 0; x <= t / 2; ++x)
+                    for (int x = 0; x <= t / 2; ++x) {
 #pragma unroll
-                        for (int y = 0; y < AHEAD; ++y)
-                            pf[t % 2][x][y] = read16(&lds.p[y][Shape::p_at(16 * t + l16, 32 * x + 8 * g)]);
+                        for (int y = 0; y + 1 < NP; ++y) pf[t % 2][x][y] = read_p(t, x, y);
+                        if constexpr (!LATE) rest[t % 2][x] = read_p(t, x, NP - 1);
+                    }
                 };
                 fetch_p(0);
                 unroll<CT>([&](auto tile) {
@@ -789,15 +793,14 @@ void chunk_kernel(const Params p) {
                         O[t][c] *= pe[t % 2];
 #pragma unroll
                         for (int x = 0; x <= t / 2; ++x)
-                            O[t][c] = mma_parts<2>(R[c][x], pf[t % 2][x], O[t][c]);
+                            O[t][c] = mma_parts<NP - 1>(R[c][x], pf[t % 2][x], O[t][c]);
                     }
-                    if constexpr (AHEAD < NP)
 #pragma unroll
-                        for (int x = 0; x <= t / 2; ++x) {
-                            const u32x4 rest = read16(&lds.p[NP - 1][Shape::p_at(16 * t + l16, 32 * x + 8 * g)]);
+                    for (int x = 0; x <= t / 2; ++x) {
+                        if constexpr (LATE) rest[t % 2][x] = read_p(t, x, NP - 1);
 #pragma unroll
-                            for (int c = 0; c < NC; ++c) O[t][c] = mma(R[c][x][0], rest, O[t][c]);
-                        }
+                        for (int c = 0; c < NC; ++c) O[t][c] = mma(R[c][x][0], rest[t % 2][x], O[t][c]);
+                    }
                 });
                 if constexpr (WIDE) {
                     const Rsrc ro = range_of(out, n * os);
