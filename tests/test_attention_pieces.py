@@ -77,6 +77,35 @@ def test_the_shape_has_sequences_whose_last_piece_ends_first(delta, piece):
     assert inverted(piece, 64) > 0
 
 
+def touched(launch, j, count):
+    """(places read, places written) by the workgroup of piece j of a continued sequence of `count`
+    pieces: its slot, and the pieces' places in the workspace."""
+    last = j + 1 == count
+    if launch == "ends":
+        if count == 1:
+            return set(), set()
+        return {"slot"} if j == 0 or last else set(), {j}
+    if launch == "out":
+        enters = "slot" if count == 1 else count - 1 if j == 0 else j - 1
+        return {enters}, {"slot"} if last else set()
+
+
+@pytest.mark.parametrize("count", range(1, 8))
+def test_no_piece_reads_what_another_of_its_launch_writes(count):
+    holds = {"slot": "entering"}  # what a place has, by the launches that ran
+    for launch in ("ends", "out"):
+        pieces = [touched(launch, j, count) for j in range(count)]
+        for i, (read, _) in enumerate(pieces):
+            for j, (_, written) in enumerate(pieces):
+                assert i == j or not read & written, (launch, i, j)
+        if launch == "ends":
+            assert all("slot" not in written for _, written in pieces)
+            holds.update({j: "entering" if j + 1 == count else f"after {j}" for j in range(count) if count > 1})
+        else:
+            for j, (read, _) in enumerate(pieces):
+                assert [holds[x] for x in read] == ["entering" if j == 0 else f"after {j - 1}"]
+
+
 # ------------------------------------------------------------------------- the GPU
 
 def problem(delta, io, st):
